@@ -5,8 +5,9 @@ lengths):
 
 * latent attention: one shared row [c_t (R) ; k_rope_t (Dr)] a token; every
   head's key is [W_uk_h c_t ; k_rope_t] and its value W_uv_h c_t. The absorbed
-  form (decode, verification of draft tokens) attends to the latent rows
-  themselves, the expanded form (prefill chunks) builds keys and values first.
+  form (decode, verification of draft tokens) takes queries that hold W_uk
+  already and attends to the latent rows themselves, with outputs in the latent
+  space; the expanded form (prefill chunks) builds keys and values first.
 * eviction: the attention weight each cached token receives is added up
   (`accumulate`), and the tokens with the least are dropped (`evict`).
 
@@ -148,8 +149,7 @@ def prepare(case, seed):
     gen = torch.Generator(device="cuda").manual_seed(1000003 * seed + 17)
     lens = _lens(case)
     table, pool = _tables(case, lens, gen)
-    st = dict(case=case, table=table, ctx=torch.from_numpy(lens.astype(np.int32)).cuda(), max_ctx=int(lens.max()),
-              lens=[int(x) for x in lens])
+    st = dict(case=case, table=table, ctx=torch.from_numpy(lens.astype(np.int32)).cuda(), max_ctx=int(lens.max()))
     return {"latent": _prepare_latent, "accumulate": _prepare_accumulate, "evict": _prepare_evict}[case["op"]](
         st, case, lens, pool, gen)
 
@@ -157,18 +157,25 @@ def prepare(case, seed):
 def _prepare_latent(st, case, lens, pool, gen):
     B, C, H, R, Dn, Dv = (case[k] for k in ("batch", "queries", "heads", "latent", "nope", "v"))
     st["cache"] = _normal((pool, case["block"], R + ROPE), gen)     # normed latents, rotated keys
-    st["q"] = _normal((B * C, H, Dn + ROPE), gen, scale=2.0)
-    st["w_uk"] = _normal((H, Dn, R), gen, scale=R ** -0.5)
-    st["w_uv"] = _normal((H, Dv, R), gen, scale=R ** -0.5)
+    if case["form"] == "absorbed":   # W_uk^T q has sqrt(Dn / R) of q's spread
+        st["q"] = _normal((B * C, H, R + ROPE), gen, scale=2.0)
+        st["q"][..., :R] *= (Dn / R) ** 0.5
+    else:
+        st["q"] = _normal((B * C, H, Dn + ROPE), gen, scale=2.0)
+        st["w_uk"] = _normal((H, Dn, R), gen, scale=R ** -0.5)
+        st["w_uv"] = _normal((H, Dv, R), gen, scale=R ** -0.5)
     st["new"] = _normal((B * C, R + ROPE), gen)                     # the rows this pass appends
     st["scale"] = (Dn + ROPE) ** -0.5
     st["before"] = torch.from_numpy((lens - C).astype(np.int32)).cuda()
     st["start"] = torch.arange(0, B * C + 1, C, dtype=torch.int32, device="cuda")
-    st["out"] = torch.empty((B * C, H, Dv), dtype=torch.bfloat16, device="cuda")
+    st["out"] = torch.empty((B * C, H, R if case["form"] == "absorbed" else Dv), dtype=torch.bfloat16, device="cuda")
     st["lse"] = torch.empty((B * C, H), dtype=torch.float32, device="cuda")
     if own:
         from paged_kv_decode_kf_gb300 import kf
-        st["ws"] = kf.make_latent_workspace(B, B * C, C, st["max_ctx"], H, R, ROPE, Dn, Dv, case["form"])
+        if case["form"] == "absorbed":
+            st["ws"] = kf.make_latent_workspace(B, C, H, R)
+        else:
+            st["ws"] = kf.make_latent_expanded_workspace(B, B * C, st["max_ctx"], H, Dn, Dv)
     return st
 
 
@@ -184,15 +191,9 @@ def _prepare_accumulate(st, case, lens, pool, gen):
     st["scores"] = torch.rand((B, st["max_ctx"]), generator=gen, device="cuda")
     st["out"] = torch.zeros((B, st["max_ctx"]), device="cuda")
     # the log-sum-exp of each row, as the attention call before it returns it
-    lse = torch.empty((B * C, Hq), device="cuda")
-    for b, L in enumerate(st["lens"]):
-        k = _rows(st["k"], st["table"], b, L).float()
-        if case["kv"] == "fp8":
-            k = k * st["k_scale"][:, None]
-        s = torch.einsum("chgd,thd->hgct", st["q"][b * C:(b + 1) * C].float().view(C, Hkv, Hq // Hkv, D), k)
-        s = (s * st["scale"]).masked_fill(_hidden(C, L), -math.inf)
-        lse[b * C:(b + 1) * C] = torch.logsumexp(s, -1).permute(2, 0, 1).reshape(C, Hq)
-    st["lse"] = lse
+    s, hidden = _scores(st)
+    lse = torch.logsumexp(s.masked_fill_(hidden[:, None, None], -math.inf), -1)
+    st["lse"] = lse.permute(0, 3, 1, 2).reshape(B * C, Hq).contiguous()
     return st
 
 
@@ -221,20 +222,21 @@ def _prepare_evict(st, case, lens, pool, gen):
 # One pass
 # ---------------------------------------------------------------------------
 
-def _slots(table, b, L, bs, first=0):
-    """Row numbers, in the pool seen as one list of rows, of tokens [first, L) of request b."""
-    t = torch.arange(first, L, device=table.device)
-    return table[b, t // bs].long() * bs + t % bs
+def _slots(table, t, bs):
+    """Row numbers of tokens t [B, n] in the pool seen as one list of rows (padding reads block 0)."""
+    return table.gather(1, t // bs).clamp_min(0).long() * bs + t % bs
 
 
-def _rows(cache, table, b, L):
-    return cache.flatten(0, 1)[_slots(table, b, L, cache.shape[1])]
+def _rows(cache, table, n):
+    """The first n rows of every request, [B, n, ...]; those past a request's length are masked later."""
+    t = torch.arange(n, device="cuda").expand(table.shape[0], n)
+    return cache.flatten(0, 1)[_slots(table, t, cache.shape[1])]
 
 
-def _hidden(C, L):
-    """[C, L] true where query j of the last C tokens must not see token t."""
-    j = torch.arange(C, device="cuda")[:, None]
-    return torch.arange(L, device="cuda")[None, :] > L - C + j
+def _hidden(ctx, C, n):
+    """[B, C, n] true where query j of the last C tokens must not see token t (or there is none)."""
+    j = torch.arange(C, device="cuda")[None, :, None]
+    return torch.arange(n, device="cuda")[None, None, :] > ctx.long()[:, None, None] - C + j
 
 
 def run(state):
@@ -243,44 +245,60 @@ def run(state):
 
 def _run_latent(st):
     case = st["case"]
-    B, C, R, Dn = case["batch"], case["queries"], case["latent"], case["nope"]
+    B, C, H, R, Dn, Dv = (case[k] for k in ("batch", "queries", "heads", "latent", "nope", "v"))
     if own:
         from paged_kv_decode_kf_gb300 import kf
         kf.kf_append_latent(st["new"], st["cache"], st["table"], st["before"], row_start=st["start"])
-        kf.kf_latent_attention(st["q"], st["cache"], st["w_uk"], st["w_uv"], st["table"], st["ctx"], st["max_ctx"],
-                               st["scale"], st["ws"], q_start=st["start"], max_query_len=C, causal=True,
-                               form=case["form"], out=st["out"], lse_out=st["lse"])
+        if case["form"] == "absorbed":
+            kf.kf_latent_attention(st["q"], st["cache"], st["table"], st["ctx"], st["max_ctx"], st["scale"], st["ws"],
+                                   q_start=st["start"], max_query_len=C, causal=True, out=st["out"],
+                                   lse_out=st["lse"])
+        else:
+            kf.kf_latent_attention_expanded(st["q"], st["cache"], st["w_uk"], st["w_uv"], st["table"], st["ctx"],
+                                            st["max_ctx"], st["scale"], st["ws"], q_start=st["start"],
+                                            max_query_len=C, causal=True, out=st["out"], lse_out=st["lse"])
         return st["out"], st["lse"]
-    wk, wv = st["w_uk"].float(), st["w_uv"].float()
-    for b, L in enumerate(st["lens"]):
-        flat = st["cache"].flatten(0, 1)
-        flat[_slots(st["table"], b, L, case["block"], L - C)] = st["new"][b * C:(b + 1) * C]
-        row = _rows(st["cache"], st["table"], b, L).float()
-        c, kr = row[:, :R], row[:, R:]
-        q = st["q"][b * C:(b + 1) * C].float()
-        if case["form"] == "absorbed":
-            ql = torch.einsum("jhn,hnr->hjr", q[..., :Dn], wk)
-            s = torch.matmul(ql, c.t()) + torch.matmul(q[..., Dn:].transpose(0, 1), kr.t())
-        else:
-            k = torch.einsum("tr,hnr->htn", c, wk)
-            s = torch.matmul(q[..., :Dn].transpose(0, 1), k.transpose(1, 2)) + \
-                torch.matmul(q[..., Dn:].transpose(0, 1), kr.t())
-        s = s.mul_(st["scale"]).masked_fill_(_hidden(C, L), -math.inf)
-        m = s.amax(-1, keepdim=True)
-        p = torch.exp(s.sub_(m))
-        l = p.sum(-1, keepdim=True)
-        if case["form"] == "absorbed":
-            o = torch.einsum("hjr,hvr->jhv", torch.matmul(p, c) / l, wv)
-        else:
-            o = (torch.matmul(p, torch.einsum("tr,hvr->htv", c, wv)) / l).transpose(0, 1)
-        st["out"][b * C:(b + 1) * C] = o.to(torch.bfloat16)
-        st["lse"][b * C:(b + 1) * C] = (m + torch.log(l))[..., 0].t()
+    M, N = st["max_ctx"], R if case["form"] == "absorbed" else Dn
+    t = st["before"].long()[:, None] + torch.arange(C, device="cuda")
+    st["cache"].flatten(0, 1)[_slots(st["table"], t, case["block"]).flatten()] = st["new"]
+    row = _rows(st["cache"], st["table"], M).float()                       # [B, M, R + 64]
+    c, kr = row[..., :R], row[..., R:]
+    q = st["q"].float().view(B, C, H, N + ROPE).transpose(1, 2)            # [B, H, C, N + 64]
+    if case["form"] == "absorbed":
+        s = torch.matmul(q.reshape(B, H * C, R + ROPE), row.transpose(1, 2)).view(B, H, C, M)
+    else:
+        s = torch.matmul(q[..., :N], torch.einsum("btr,hnr->bhnt", c, st["w_uk"].float()))
+        s += torch.matmul(q[..., N:].reshape(B, H * C, ROPE), kr.transpose(1, 2)).view(B, H, C, M)
+    s = s.mul_(st["scale"]).masked_fill_(_hidden(st["ctx"], C, M)[:, None], -math.inf)
+    m = s.amax(-1, keepdim=True)
+    p = s.sub_(m).exp_()
+    l = p.sum(-1, keepdim=True)
+    if case["form"] == "absorbed":
+        o = torch.matmul(p.view(B, H * C, M), c).view(B, H, C, R)
+    else:
+        o = torch.matmul(p, torch.einsum("btr,hvr->bhtv", c, st["w_uv"].float()))
+    o = (o / l).transpose(1, 2)
+    st["out"].copy_(o.reshape(st["out"].shape))
+    st["lse"].copy_((m + torch.log(l))[..., 0].transpose(1, 2).reshape(B * C, H))
     return st["out"], st["lse"]
+
+
+def _scores(st):
+    """Scaled scores [B, Hkv, G, C, M] in fp32 and the mask [B, C, M] of what is not seen."""
+    case = st["case"]
+    B, C, Hq, Hkv, D = (case[k] for k in ("batch", "queries", "q_heads", "kv_heads", "dim"))
+    M = st["max_ctx"]
+    k = _rows(st["k"], st["table"], M).float()
+    if case["kv"] == "fp8":
+        k = k.mul_(st["k_scale"][:, None])
+    q = st["q"].float().view(B, C, Hkv, Hq // Hkv, D).permute(0, 2, 3, 1, 4).reshape(B, Hkv, -1, D)
+    s = torch.matmul(q, k.permute(0, 2, 3, 1)).mul_(st["scale"]).view(B, Hkv, Hq // Hkv, C, M)
+    return s, _hidden(st["ctx"], C, M)
 
 
 def _run_accumulate(st):
     case = st["case"]
-    C, Hq, Hkv, D = case["queries"], case["q_heads"], case["kv_heads"], case["dim"]
+    B, C, Hq, Hkv = (case[k] for k in ("batch", "queries", "q_heads", "kv_heads"))
     if own:
         from paged_kv_decode_kf_gb300 import kf
         extra = dict(q_start=st["start"], max_query_len=C) if C > 1 else {}
@@ -291,15 +309,11 @@ def _run_accumulate(st):
             kf.kf_accumulate_attention(st["q"], st["k"], st["table"], st["ctx"], st["max_ctx"], st["scale"],
                                        st["lse"], st["out"], scores_in=st["scores"], **extra)
         return st["out"]
-    for b, L in enumerate(st["lens"]):
-        k = _rows(st["k"], st["table"], b, L).float()
-        if case["kv"] == "fp8":
-            k = k * st["k_scale"][:, None]
-        q = st["q"][b * C:(b + 1) * C].float().view(C, Hkv, Hq // Hkv, D).permute(1, 2, 0, 3).reshape(Hkv, -1, D)
-        lse = st["lse"][b * C:(b + 1) * C].view(C, Hkv, Hq // Hkv).permute(1, 2, 0)
-        s = torch.matmul(q, k.permute(1, 2, 0)).mul_(st["scale"]).view(Hkv, Hq // Hkv, C, L)
-        w = torch.exp(s.sub_(lse[..., None])).masked_fill_(_hidden(C, L), 0.0)
-        st["out"][b, :L] = st["scores"][b, :L] + w.sum((0, 1, 2))
+    s, hidden = _scores(st)
+    lse = st["lse"].view(B, C, Hkv, Hq // Hkv).permute(0, 2, 3, 1)
+    w = s.sub_(lse[..., None]).exp_().masked_fill_(hidden[:, None, None], 0.0).sum((1, 2, 3))
+    live = torch.arange(st["max_ctx"], device="cuda") < st["ctx"][:, None]
+    st["out"].copy_(torch.where(live, st["scores"] + w, st["out"]))
     return st["out"]
 
 
@@ -313,30 +327,32 @@ def _run_evict(st):
                            st["ctx_out"], st["scores_out"], st["ws"], positions=st.get("positions"),
                            seq_lens=st.get("seen"), positions_out=st.get("positions_out"))
     else:
-        for b, L in enumerate(st["lens"]):
-            n = min(L, keep)
-            sc = st["scores"][b, :L]
-            pos = st["positions"][b, :L] if pos_on else torch.arange(L, device="cuda")
-            if L > keep:
-                seen = st["seen"][b] if pos_on else L
-                prot = (pos < sink) | (pos >= seen - recent)
-                order = torch.argsort(torch.where(prot, math.inf, sc), descending=True, stable=True)
-                kept = torch.zeros(L, dtype=torch.bool, device="cuda")
-                kept[order[:keep]] = True
-                dst = torch.nonzero(~kept[:keep])[:, 0]
-                src = torch.nonzero(kept[keep:])[:, 0] + keep
-                for cache in st["caches"]:
-                    flat = cache.flatten(0, 1)
-                    flat[st["table"][b, dst // bs].long() * bs + dst % bs] = \
-                        flat[st["table"][b, src // bs].long() * bs + src % bs]
-                idx = torch.arange(keep, device="cuda")
-                idx[dst] = src
-            else:
-                idx = torch.arange(L, device="cuda")
-            st["scores_out"][b, :n] = sc[idx]
-            if pos_on:
-                st["positions_out"][b, :n] = pos[idx]
-            st["ctx_out"][b] = n
+        M = st["max_ctx"]
+        K = min(keep, M)
+        t = torch.arange(M, device="cuda").expand(case["batch"], M)
+        L = st["ctx"].long()[:, None]
+        live = t < L
+        pos, seen = (st["positions"], st["seen"].long()[:, None]) if pos_on else (t, L)
+        # protected first, then by weight, the lower index first among equals; padding last
+        key = torch.where((pos < sink) | (pos >= seen - recent), math.inf, st["scores"])
+        order = torch.argsort(torch.where(live, key, -math.inf), dim=1, descending=True, stable=True)
+        kept = torch.zeros_like(live).scatter_(1, order[:, :K], True) & live
+        # the holes below `keep` take the kept tokens above it, both in order
+        dst = torch.nonzero(~kept[:, :K] & (L > keep))
+        src = torch.nonzero(kept[:, K:])
+        db, dt, st_ = dst[:, 0], dst[:, 1], src[:, 1] + K
+        at_d = st["table"][db, dt // bs].long() * bs + dt % bs
+        at_s = st["table"][db, st_ // bs].long() * bs + st_ % bs
+        for cache in st["caches"]:
+            flat = cache.flatten(0, 1)
+            flat[at_d] = flat[at_s]
+        idx = t[:, :K].clone()
+        idx[db, dt] = st_
+        fits = t[:, :K] < L
+        st["scores_out"][:, :K] = torch.where(fits, st["scores"].gather(1, idx), st["scores_out"][:, :K])
+        if pos_on:
+            st["positions_out"][:, :K] = torch.where(fits, pos.gather(1, idx), st["positions_out"][:, :K])
+        st["ctx_out"].copy_(st["ctx"].clamp_max(keep))
     out = dict(ctx=st["ctx_out"], scores=st["scores_out"])
     for i, cache in enumerate(st["caches"]):
         out["cache%d" % i] = cache
@@ -357,11 +373,13 @@ def work(case):
         rows = B * C
         # (query, token) pairs under the causal mask
         pairs = float((lens * C).sum() - B * C * (C - 1) / 2)
-        data = tokens * (R + ROPE) * 2 + H * R * (Dn + Dv) * 2 + rows * H * ((Dn + ROPE + Dv) * 2 + 4) + \
-            rows * (R + ROPE) * 2
+        # the appended rows are read where they are given and written; attention may read them there too
+        data = tokens * (R + ROPE) * 2 + rows * (R + ROPE) * 2
         if case["form"] == "absorbed":
-            flops = 2.0 * pairs * H * (2 * R + ROPE) + 2.0 * rows * H * R * (Dn + Dv)
+            data += rows * H * ((2 * R + ROPE) * 2 + 4)
+            flops = 2.0 * pairs * H * (2 * R + ROPE)
         else:
+            data += rows * H * ((Dn + ROPE + Dv) * 2 + 4) + H * R * (Dn + Dv) * 2
             flops = 2.0 * pairs * H * (Dn + ROPE + Dv) + 2.0 * tokens * H * R * (Dn + Dv)
         return {"bytes": data, "flops": flops}
     if case["op"] == "accumulate":
@@ -409,10 +427,10 @@ def _token_rows(cache, table, b, L):
 
 def _exact_latent(case, st, lens):
     """Head by head from the definition: keys and values of one head, then its softmax."""
-    B, C, H, R, Dn, Dv = (case[k] for k in ("batch", "queries", "heads", "latent", "nope", "v"))
-    out = torch.zeros((B * C, H, Dv), dtype=torch.float64, device="cuda")
-    lse = torch.zeros((B * C, H), dtype=torch.float64, device="cuda")
+    B, C, H, R, Dn = (case[k] for k in ("batch", "queries", "heads", "latent", "nope"))
     absorbed = case["form"] == "absorbed"
+    out = torch.zeros(st["out"].shape, dtype=torch.float64, device="cuda")
+    lse = torch.zeros((B * C, H), dtype=torch.float64, device="cuda")
     for b in range(B):
         L = int(lens[b])
         row = _token_rows(st["cache"], st["table"], b, L).double()
@@ -421,15 +439,15 @@ def _exact_latent(case, st, lens):
         seen = torch.arange(L, device="cuda")[None, :] <= last[:, None]
         for h in range(H):
             q = st["q"][b * C:(b + 1) * C, h].double()
-            wk, wv = st["w_uk"][h].double(), st["w_uv"][h].double()
-            if absorbed:   # fewer products for few queries; the same numbers in 64 bits
-                s = torch.cat([q[:, :Dn] @ wk, q[:, Dn:]], 1) @ row.t() * st["scale"]
+            if absorbed:
+                key, value = row, row[:, :R]
             else:
-                s = q @ torch.cat([row[:, :R] @ wk.t(), row[:, R:]], 1).t() * st["scale"]
+                key = torch.cat([row[:, :R] @ st["w_uk"][h].double().t(), row[:, R:]], 1)
+                value = row[:, :R] @ st["w_uv"][h].double().t()
+            s = q @ key.t() * st["scale"]
             s = torch.where(seen, s, torch.full_like(s, -math.inf))
             lse[b * C:(b + 1) * C, h] = torch.logsumexp(s, 1)
-            p = torch.softmax(s, 1)
-            out[b * C:(b + 1) * C, h] = (p @ row[:, :R]) @ wv.t() if absorbed else p @ (row[:, :R] @ wv.t())
+            out[b * C:(b + 1) * C, h] = torch.softmax(s, 1) @ value
     return out, lse
 
 
