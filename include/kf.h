@@ -89,6 +89,7 @@ typedef enum { KF_BF16 = 0, KF_F32 = 1 } kf_dtype;
 #define KF_DEVERR_MAX_CONTEXT 0x04u /* a context length above max_context_len */
 #define KF_DEVERR_APPEND_POS  0x08u /* an append position outside the block table */
 #define KF_DEVERR_TIMEOUT     0x10u /* a pipeline wait in a kernel gave up */
+#define KF_DEVERR_RANGE       0x20u /* an expanded value outside fp16's range */
 
 /*
  * kf_append_kv -- write the step's new K/V row of every request into the cache.
@@ -443,6 +444,224 @@ kf_status kf_decode_step_static(const void *q, const void *k_new, const void *v_
                                 int num_q_heads, int num_kv_heads, int head_dim, int block_size,
                                 int64_t num_blocks, float scale, int num_splits, void *out,
                                 kf_dtype out_dtype, float *lse_out, kf_stream_t stream);
+
+/*
+ * Latent attention: kf_append_latent, kf_latent_attention,
+ * kf_latent_attention_expanded.
+ *
+ * A latent cache keeps one row a token that all heads share: [c_t (latent_dim) ;
+ * r_t (rope_dim)] in bf16, [num_blocks, block_size, latent_dim + rope_dim], read
+ * through the same block tables as the K/V caches. Head h's key of token t is
+ * [W_uk_h c_t ; r_t] and its value W_uv_h c_t, so that for a query [q_n ; q_r]
+ *   s_t = scale * (<q_n, W_uk_h c_t> + <q_r, r_t>),  p = softmax over the tokens seen,
+ *   out = sum_t p_t W_uv_h c_t,  lse = ln sum_t e^{s_t}.
+ * Because <q_n, W_uk_h c_t> = <W_uk_h^T q_n, c_t> and W_uv_h is linear, the same
+ * result comes from two forms:
+ *  - absorbed (kf_latent_attention): the caller's queries are [W_uk_h^T q_n ; q_r]
+ *    (latent_dim + rope_dim wide) and its outputs sum_t p_t c_t (latent_dim
+ *    wide); the two per-head products with W_uk and W_uv are the caller's own
+ *    matrix products. Reads (latent_dim + rope_dim) * 2 bytes a token for all
+ *    heads: decode, and verification of a few draft tokens.
+ *  - expanded (kf_latent_attention_expanded): keys and values of every cached
+ *    token are built in the workspace, then attended to, at less than a third
+ *    of the arithmetic a (query, token) pair: prefill chunks (it pays from a
+ *    chunk of about 170 queries on at latent_dim 512, nope_dim = v_dim = 128).
+ *
+ * Shapes: latent_dim 256 or 512, rope_dim 64, block_size 16 or 32, num_heads
+ * from 1 to 1024. Conventions, errors and device errors as the other calls
+ * (host pointers are not taken); every device pointer is 16-byte aligned but
+ * for int32 and f32 arrays of one element per row, table entry or request,
+ * which need 4 bytes.
+ */
+
+/*
+ * kf_append_latent -- write new latent rows of every request into the cache.
+ *
+ * Request b's rows, row_start[b] .. row_start[b+1]-1 of latent_new, go to
+ * positions context_lens_before[b], context_lens_before[b] + 1, ... in order;
+ * the copy is bit-exact and no other byte of the cache is written. row_start
+ * NULL: one row a request (num_rows == batch).
+ *
+ *   latent_new           bf16 [num_rows, latent_dim + rope_dim]
+ *   row_start            int32 [batch + 1] (device), ascending, or NULL; rows
+ *                        outside [row_start[0], row_start[batch]) are not used
+ *   latent_cache         bf16 [num_blocks, block_size, latent_dim + rope_dim] (written)
+ *   context_lens_before  int32 [batch], tokens cached before this call (not modified)
+ *
+ * Device errors as kf_append_kv, a row at a time; row_start that does not
+ * ascend -> KF_DEVERR_CONTEXT_LEN (those rows are not written).
+ */
+kf_status kf_append_latent(const void *latent_new, const int32_t *row_start, void *latent_cache,
+                           const int32_t *block_tables, int bt_stride,
+                           const int32_t *context_lens_before, int batch, int num_rows,
+                           int latent_dim, int rope_dim, int block_size, int64_t num_blocks,
+                           kf_stream_t stream);
+
+/*
+ * kf_latent_attention -- latent attention in the absorbed form.
+ *
+ *   q             bf16 [num_q_tokens, num_heads, latent_dim + rope_dim]
+ *   q_start       int32 [batch + 1] (device), ascending: request b owns query
+ *                 tokens q_start[b] .. q_start[b+1]-1 (C_b of them), the last C_b
+ *                 of its context_lens[b] cached tokens; or NULL: one query token a
+ *                 request (num_q_tokens == batch)
+ *   context_lens  int32 [batch], tokens in the cache, the queries' own included
+ *   causal        1: query j sees tokens [0, L_b - C_b + j]; 0: all L_b tokens
+ *   max_context_len, max_query_len  host-side bounds of L_b and C_b
+ *   workspace     device scratch of kf_latent_workspace_size() bytes, 16-byte
+ *                 aligned, any contents. Calls that share one must not overlap
+ *                 on the GPU.
+ *   out           [num_q_tokens, num_heads, latent_dim] of out_dtype
+ *   lse_out       f32 [num_q_tokens, num_heads], or NULL
+ *
+ * A row that sees no token (an empty request, or the first C_b - L_b queries of
+ * a causal call with C_b > L_b) gives out = 0 and lse = -inf. Rows of q that no
+ * request owns are left as they were in out and lse_out. Scores, softmax
+ * statistics and sums are fp32; the softmax weights enter the value product as
+ * bf16 (the cache's type), the sum that normalises them does not.
+ * Host errors as kf_paged_multiquery_attention; a missing or short workspace ->
+ * KF_ERR_INVALID. Device errors: KF_DEVERR_BLOCK_ID; KF_DEVERR_CONTEXT_LEN (a
+ * length out of range; query ranges outside q: that request is left out); KF_DEVERR_MAX_CONTEXT (lengths above the host bounds:
+ * what lies above them is left out).
+ */
+kf_status kf_latent_attention(const void *q, const int32_t *q_start, const void *latent_cache,
+                              const int32_t *block_tables, int bt_stride,
+                              const int32_t *context_lens, int causal, int max_context_len,
+                              int max_query_len, int batch, int num_q_tokens, int num_heads,
+                              int latent_dim, int rope_dim, int block_size, int64_t num_blocks,
+                              float scale, void *workspace, size_t workspace_bytes, void *out,
+                              kf_dtype out_dtype, float *lse_out, kf_stream_t stream);
+
+/* Workspace bytes of kf_latent_attention on the CURRENT device; 0 if that device
+ * cannot be queried or the arguments are invalid. */
+size_t kf_latent_workspace_size(int batch, int max_query_len, int num_heads, int latent_dim);
+
+/*
+ * kf_latent_attention_expanded -- latent attention in the expanded form.
+ *
+ * Arguments as kf_latent_attention, with
+ *   q          bf16 [num_q_tokens, num_heads, nope_dim + rope_dim]
+ *   w_uk       bf16 [num_heads, nope_dim, latent_dim]
+ *   w_uv       bf16 [num_heads, v_dim, latent_dim]
+ *   out        [num_q_tokens, num_heads, v_dim] of out_dtype
+ *   workspace  of kf_latent_expanded_workspace_size() bytes, 16-byte aligned, any
+ *              contents
+ * nope_dim = v_dim = 64 or 128. Expanded keys enter the score products as pairs
+ * of bf16 numbers (together 16 bits of significand, so that lse stays as exact
+ * as in the absorbed form), values and softmax weights the value product as
+ * fp16 (a rounding an eighth of bf16's); an expanded value above fp16's largest
+ * number (65504) sets KF_DEVERR_RANGE and leaves that request's outputs
+ * unspecified.
+ */
+kf_status kf_latent_attention_expanded(const void *q, const int32_t *q_start,
+                                       const void *latent_cache, const void *w_uk,
+                                       const void *w_uv, const int32_t *block_tables,
+                                       int bt_stride, const int32_t *context_lens, int causal,
+                                       int max_context_len, int max_query_len, int batch,
+                                       int num_q_tokens, int num_heads, int latent_dim,
+                                       int rope_dim, int nope_dim, int v_dim, int block_size,
+                                       int64_t num_blocks, float scale, void *workspace,
+                                       size_t workspace_bytes, void *out, kf_dtype out_dtype,
+                                       float *lse_out, kf_stream_t stream);
+
+/* Workspace bytes of kf_latent_attention_expanded; 0 if the arguments are invalid. */
+size_t kf_latent_expanded_workspace_size(int batch, int num_q_tokens, int max_context_len,
+                                         int num_heads, int nope_dim, int v_dim);
+
+/*
+ * Eviction by accumulated attention weight: kf_accumulate_attention[_fp8],
+ * kf_evict_tokens.
+ *
+ * A cache bounded to `keep` tokens a request drops the tokens that later
+ * queries have looked at least. kf_accumulate_attention adds up, per cached
+ * token, the softmax weight it received; kf_evict_tokens picks who stays and
+ * closes the gaps in place, for any paged cache (K/V in bf16 or E4M3, latent).
+ */
+
+/*
+ * kf_accumulate_attention -- the attention weight each cached token receives.
+ *
+ *   scores_out[b, t] = scores_in[b, t] + sum_{j sees t} sum_h e^{scale <q_jh, k_{h/G,t}> - lse_jh}
+ * for the tokens t < context_lens[b]; entries at and above that are not
+ * written. q and q_start as kf_paged_multiquery_attention (q_start NULL: one
+ * query token a request); lse is what the attention call over the same queries
+ * returned, so that the weights are those of that call (with extra partials
+ * merged, say, weights of the whole). A row whose lse is -inf adds nothing. Each
+ * sum runs in one fixed order: equal calls give equal bits.
+ *
+ *   lse         f32 [num_q_tokens, num_q_heads]
+ *   scores_in   f32 [batch, score_stride], or NULL for zeros
+ *   scores_out  f32 [batch, score_stride]; may be scores_in
+ *   score_stride >= max_context_len
+ *
+ * Host errors as kf_paged_multiquery_attention, plus score_stride <
+ * max_context_len -> KF_ERR_INVALID. Device errors as kf_latent_attention.
+ * The _fp8 call reads an E4M3 key cache with k_scale f32 [num_kv_heads].
+ */
+kf_status kf_accumulate_attention(const void *q, const int32_t *q_start, const void *k_cache,
+                                  const int32_t *block_tables, int bt_stride,
+                                  const int32_t *context_lens, int causal, int max_context_len,
+                                  int max_query_len, int batch, int num_q_tokens, int num_q_heads,
+                                  int num_kv_heads, int head_dim, int block_size,
+                                  int64_t num_blocks, float scale, const float *lse,
+                                  const float *scores_in, float *scores_out, int64_t score_stride,
+                                  kf_stream_t stream);
+
+kf_status kf_accumulate_attention_fp8(const void *q, const int32_t *q_start, const void *k_cache,
+                                      const float *k_scale, const int32_t *block_tables,
+                                      int bt_stride, const int32_t *context_lens, int causal,
+                                      int max_context_len, int max_query_len, int batch,
+                                      int num_q_tokens, int num_q_heads, int num_kv_heads,
+                                      int head_dim, int block_size, int64_t num_blocks,
+                                      float scale, const float *lse, const float *scores_in,
+                                      float *scores_out, int64_t score_stride,
+                                      kf_stream_t stream);
+
+/*
+ * kf_evict_tokens -- cut every request's cache to its `keep` tokens of most
+ * weight, in place.
+ *
+ * Of a request's L = context_lens[b] tokens the first min(L, keep) in this
+ * order stay: protected tokens, then larger scores, then lower indices (-0 = +0;
+ * NaN ranks below -inf). Protected are positions below `sink` and the `recent`
+ * positions before the sequence's length. A kept token at an index below `keep`
+ * stays in its slot; the i-th kept token (in index order) at or above `keep`
+ * moves into the i-th evicted slot below it. Rows, scores and positions move
+ * alike; attention does not depend on the order of cached tokens. The request
+ * then holds min(L, keep) tokens; blocks past them are the caller's to free.
+ *
+ *   cache_a, cache_b  caches of rows of row_bytes bytes, [num_blocks, block_size]
+ *                     rows (K and V; or one latent cache, cache_b NULL). The rows
+ *                     moved into must not be shared with another request.
+ *   scores            f32 [batch, score_stride]
+ *   scores_out        f32 [batch, score_stride], entries [0, min(L, keep)) written;
+ *                     may be scores
+ *   positions         int32 [batch, score_stride], each cached token's position in
+ *                     its sequence, with seq_lens int32 [batch] (tokens of the
+ *                     sequence so far) and positions_out (may be positions); or
+ *                     all three NULL: a token's position is its index, and the
+ *                     sequence's length is L
+ *   keep >= 1, sink + recent <= keep
+ *   context_lens_out  int32 [batch]; may be context_lens
+ *   workspace         kf_evict_workspace_size() bytes, 16-byte aligned, any contents
+ *
+ * Host errors: null pointers, sizes out of range, part of the three position
+ * arrays -> KF_ERR_INVALID; row_bytes not a multiple of 16 (or above 1 MiB),
+ * block_size other than 16 or 32 -> KF_ERR_UNSUPPORTED. Device errors:
+ * KF_DEVERR_CONTEXT_LEN, KF_DEVERR_MAX_CONTEXT (tokens at and above
+ * max_context_len are dropped), KF_DEVERR_BLOCK_ID (that row does not move).
+ */
+kf_status kf_evict_tokens(void *cache_a, void *cache_b, int64_t row_bytes,
+                          const int32_t *block_tables, int bt_stride, const int32_t *context_lens,
+                          int max_context_len, int batch, int block_size, int64_t num_blocks,
+                          const float *scores, float *scores_out, int64_t score_stride,
+                          const int32_t *positions, int32_t *positions_out,
+                          const int32_t *seq_lens, int keep, int sink, int recent,
+                          int32_t *context_lens_out, void *workspace, size_t workspace_bytes,
+                          kf_stream_t stream);
+
+/* Workspace bytes of kf_evict_tokens; 0 if the arguments are invalid. */
+size_t kf_evict_workspace_size(int batch, int max_context_len, int keep);
 
 /*
  * kf_get_device_error -- read and clear the current device's error word.

@@ -103,6 +103,21 @@ void *encode_fn() {
     return g_encode_fn;
 }
 
+}  // namespace
+
+cudaError_t device_facts(unsigned int **err, int *sm_count) {
+    DeviceInfo *dev = nullptr;
+    const cudaError_t e = device_info(&dev);
+    if (e != cudaSuccess) return e;
+    *err = dev->err;
+    *sm_count = dev->sm_count;
+    return cudaSuccess;
+}
+
+void *tensor_map_encoder() { return encode_fn(); }
+
+namespace {
+
 bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 bool supported_dims(int head_dim, int block_size) {

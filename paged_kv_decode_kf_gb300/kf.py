@@ -31,6 +31,7 @@ KF_DEVERR_CONTEXT_LEN = 0x02
 KF_DEVERR_MAX_CONTEXT = 0x04
 KF_DEVERR_APPEND_POS = 0x08
 KF_DEVERR_TIMEOUT = 0x10
+KF_DEVERR_RANGE = 0x20
 
 _vp, _i32, _i64, _f32 = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_float
 
@@ -72,6 +73,31 @@ _lib.kf_decode_step_fp8.restype = _i32
 _lib.kf_decode_step_fp8.argtypes = [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i32, _vp, _i32, _i32, _i32,
                                     _i32, _i32, _i32, _i64, _f32, _i32, _vp, ctypes.c_size_t, _vp, _i32, _vp,
                                     _vp]
+_sz = ctypes.c_size_t
+_lib.kf_append_latent.restype = _i32
+_lib.kf_append_latent.argtypes = [_vp, _vp, _vp, _vp, _i32, _vp, _i32, _i32, _i32, _i32, _i32, _i64, _vp]
+_lib.kf_latent_workspace_size.restype = _sz
+_lib.kf_latent_workspace_size.argtypes = [_i32] * 4
+_lib.kf_latent_attention.restype = _i32
+_lib.kf_latent_attention.argtypes = [_vp, _vp, _vp, _vp, _i32, _vp, _i32, _i32, _i32, _i32, _i32, _i32, _i32,
+                                     _i32, _i32, _i64, _f32, _vp, _sz, _vp, _i32, _vp, _vp]
+_lib.kf_latent_expanded_workspace_size.restype = _sz
+_lib.kf_latent_expanded_workspace_size.argtypes = [_i32] * 6
+_lib.kf_latent_attention_expanded.restype = _i32
+_lib.kf_latent_attention_expanded.argtypes = [_vp, _vp, _vp, _vp, _vp, _vp, _i32, _vp, _i32, _i32, _i32, _i32,
+                                              _i32, _i32, _i32, _i32, _i32, _i32, _i32, _i64, _f32, _vp, _sz, _vp,
+                                              _i32, _vp, _vp]
+_lib.kf_accumulate_attention.restype = _i32
+_lib.kf_accumulate_attention.argtypes = [_vp, _vp, _vp, _vp, _i32, _vp, _i32, _i32, _i32, _i32, _i32, _i32, _i32,
+                                         _i32, _i32, _i64, _f32, _vp, _vp, _vp, _i64, _vp]
+_lib.kf_accumulate_attention_fp8.restype = _i32
+_lib.kf_accumulate_attention_fp8.argtypes = [_vp, _vp, _vp, _vp, _vp, _i32, _vp, _i32, _i32, _i32, _i32, _i32,
+                                             _i32, _i32, _i32, _i32, _i64, _f32, _vp, _vp, _vp, _i64, _vp]
+_lib.kf_evict_workspace_size.restype = _sz
+_lib.kf_evict_workspace_size.argtypes = [_i32] * 3
+_lib.kf_evict_tokens.restype = _i32
+_lib.kf_evict_tokens.argtypes = [_vp, _vp, _i64, _vp, _i32, _vp, _i32, _i32, _i32, _i64, _vp, _vp, _i64, _vp, _vp,
+                                 _vp, _i32, _i32, _i32, _vp, _vp, _sz, _vp]
 _lib.kf_get_device_error.restype = _i32
 _lib.kf_check_bounded_wait.restype = _i32
 _lib.kf_check_bounded_wait.argtypes = [_vp]
@@ -417,6 +443,260 @@ def kf_decode_step_fp8(q, k_new, v_new, k_cache, v_cache, k_scale, v_scale, bloc
         None if lse_out is None else _io(lse_out, torch.float32, "lse_out"), _stream(stream)),
         "kf_decode_step_fp8")
     return out, lse_out
+
+
+def _latent_dims(latent_cache: torch.Tensor) -> Tuple[int, int, int, int]:
+    """(num_blocks, block_size, latent_dim, rope_dim) of a latent cache."""
+    if latent_cache.dim() != 3 or latent_cache.shape[2] <= KF_ROPE_DIM:
+        raise ValueError("latent_cache must be [num_blocks, block_size, latent_dim + %d]" % KF_ROPE_DIM)
+    nb, bs, w = latent_cache.shape
+    return nb, bs, w - KF_ROPE_DIM, KF_ROPE_DIM
+
+
+def _shape(t: torch.Tensor, shape, name: str) -> None:
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError("%s must be %s, got %s" % (name, list(shape), list(t.shape)))
+
+
+def _same_device(first: torch.Tensor, *rest) -> torch.cuda.device:
+    """Guard that makes the tensors' device current; they must share one."""
+    for t in rest:
+        if t is not None and t.device != first.device:
+            raise ValueError("all tensors must be on %s, got one on %s" % (first.device, t.device))
+    if not first.is_cuda:
+        raise ValueError("all tensors must be CUDA tensors")
+    return torch.cuda.device(first.device)
+
+
+def _opt(t: Optional[torch.Tensor], dtype, name: str) -> Optional[int]:
+    return None if t is None else _dev(t, dtype, name)
+
+
+KF_ROPE_DIM = 64  # width of the rotary part of a latent row
+
+
+def kf_append_latent(latent_new: torch.Tensor, latent_cache: torch.Tensor, block_tables: torch.Tensor,
+                     context_lens_before: torch.Tensor, row_start: Optional[torch.Tensor] = None,
+                     stream=None) -> None:
+    """Write each request's new latent rows (one, or rows row_start[b]..row_start[b+1]-1)
+    from position context_lens_before[b] on."""
+    nb, bs, r, rope = _latent_dims(latent_cache)
+    B, n = block_tables.shape[0], latent_new.shape[0]
+    _shape(latent_new, (n, r + rope), "latent_new")
+    _shape(context_lens_before, (B,), "context_lens_before")
+    if row_start is not None:
+        _shape(row_start, (B + 1,), "row_start")
+    elif n != B:
+        raise ValueError("latent_new must hold one row a request without row_start")
+    with _same_device(latent_cache, latent_new, block_tables, context_lens_before, row_start):
+        _check(_lib.kf_append_latent(
+            _dev(latent_new, torch.bfloat16, "latent_new"), _opt(row_start, torch.int32, "row_start"),
+            _dev(latent_cache, torch.bfloat16, "latent_cache"), _dev(block_tables, torch.int32, "block_tables"),
+            block_tables.shape[1], _dev(context_lens_before, torch.int32, "context_lens_before"), B, n, r, rope, bs,
+            nb, _stream(stream)), "kf_append_latent")
+
+
+def kf_latent_workspace_size(batch: int, max_query_len: int, num_heads: int, latent_dim: int) -> int:
+    return int(_lib.kf_latent_workspace_size(batch, max_query_len, num_heads, latent_dim))
+
+
+def make_latent_workspace(batch: int, max_query_len: int, num_heads: int, latent_dim: int,
+                          device=None) -> torch.Tensor:
+    """A workspace for kf_latent_attention (any contents)."""
+    dev = torch.device(device or "cuda")
+    with torch.cuda.device(dev):
+        n = kf_latent_workspace_size(batch, max_query_len, num_heads, latent_dim)
+        return torch.empty(max(n, 16), dtype=torch.uint8, device=dev)
+
+
+def _latent_call(q, width, out_width, block_tables, context_lens, q_start, out, out_dtype, lse_out, want_lse):
+    """Shape checks and outputs shared by the two forms; returns (out, out code, lse_out)."""
+    if q.dim() != 3:
+        raise ValueError("q must be [num_q_tokens, num_heads, %d]" % width)
+    nq, h, _ = q.shape
+    _shape(q, (nq, h, width), "q")
+    B = block_tables.shape[0]
+    _shape(context_lens, (B,), "context_lens")
+    if q_start is not None:
+        _shape(q_start, (B + 1,), "q_start")
+    elif nq != B:
+        raise ValueError("q must hold one query token a request without q_start")
+    if out is None:
+        out = torch.empty((nq, h, out_width), dtype=out_dtype, device=q.device)
+    _shape(out, (nq, h, out_width), "out")
+    code = {torch.float32: KF_F32, torch.bfloat16: KF_BF16}.get(out.dtype)
+    if code is None:
+        raise ValueError("out must be float32 or bfloat16")
+    if lse_out is None and want_lse:
+        lse_out = torch.empty((nq, h), dtype=torch.float32, device=q.device)
+    if lse_out is not None:
+        _shape(lse_out, (nq, h), "lse_out")
+    return out, code, lse_out
+
+
+def kf_latent_attention(q: torch.Tensor, latent_cache: torch.Tensor, block_tables: torch.Tensor,
+                        context_lens: torch.Tensor, max_context_len: int, scale: float, workspace: torch.Tensor,
+                        q_start: Optional[torch.Tensor] = None, max_query_len: int = 1, causal: bool = True,
+                        out: Optional[torch.Tensor] = None, out_dtype=torch.bfloat16,
+                        lse_out: Optional[torch.Tensor] = None, want_lse: bool = True,
+                        stream=None) -> Tuple[torch.Tensor, Optional[torch.Tensor]]:
+    """Latent attention, absorbed form: q [Nq, H, R + 64] over the latent cache;
+    returns (out [Nq, H, R], lse [Nq, H])."""
+    nb, bs, r, rope = _latent_dims(latent_cache)
+    out, code, lse_out = _latent_call(q, r + rope, r, block_tables, context_lens, q_start, out, out_dtype, lse_out,
+                                      want_lse)
+    with _same_device(q, latent_cache, block_tables, context_lens, workspace, q_start, out, lse_out):
+        _check(_lib.kf_latent_attention(
+            _dev(q, torch.bfloat16, "q"), _opt(q_start, torch.int32, "q_start"),
+            _dev(latent_cache, torch.bfloat16, "latent_cache"), _dev(block_tables, torch.int32, "block_tables"),
+            block_tables.shape[1], _dev(context_lens, torch.int32, "context_lens"), int(bool(causal)),
+            int(max_context_len), int(max_query_len), block_tables.shape[0], q.shape[0], q.shape[1], r, rope, bs, nb,
+            float(scale), _dev(workspace, torch.uint8, "workspace"), workspace.numel(), _dev(out, out.dtype, "out"),
+            code, _opt(lse_out, torch.float32, "lse_out"), _stream(stream)), "kf_latent_attention")
+    return out, lse_out
+
+
+def kf_latent_expanded_workspace_size(batch: int, num_q_tokens: int, max_context_len: int, num_heads: int,
+                                      nope_dim: int, v_dim: int) -> int:
+    return int(_lib.kf_latent_expanded_workspace_size(batch, num_q_tokens, max_context_len, num_heads, nope_dim,
+                                                      v_dim))
+
+
+def make_latent_expanded_workspace(batch: int, num_q_tokens: int, max_context_len: int, num_heads: int,
+                                   nope_dim: int, v_dim: int, device=None) -> torch.Tensor:
+    """A workspace for kf_latent_attention_expanded (any contents)."""
+    n = kf_latent_expanded_workspace_size(batch, num_q_tokens, max_context_len, num_heads, nope_dim, v_dim)
+    return torch.empty(max(n, 16), dtype=torch.uint8, device=device or "cuda")
+
+
+def kf_latent_attention_expanded(q: torch.Tensor, latent_cache: torch.Tensor, w_uk: torch.Tensor,
+                                 w_uv: torch.Tensor, block_tables: torch.Tensor, context_lens: torch.Tensor,
+                                 max_context_len: int, scale: float, workspace: torch.Tensor,
+                                 q_start: Optional[torch.Tensor] = None, max_query_len: int = 1,
+                                 causal: bool = True, out: Optional[torch.Tensor] = None,
+                                 out_dtype=torch.bfloat16, lse_out: Optional[torch.Tensor] = None,
+                                 want_lse: bool = True, stream=None) -> Tuple[torch.Tensor, Optional[torch.Tensor]]:
+    """Latent attention, expanded form: q [Nq, H, Dn + 64], w_uk [H, Dn, R], w_uv
+    [H, Dv, R]; returns (out [Nq, H, Dv], lse [Nq, H])."""
+    nb, bs, r, rope = _latent_dims(latent_cache)
+    if w_uk.dim() != 3 or w_uv.dim() != 3:
+        raise ValueError("w_uk and w_uv must be [num_heads, width, latent_dim]")
+    dn, dv = w_uk.shape[1], w_uv.shape[1]
+    out, code, lse_out = _latent_call(q, dn + rope, dv, block_tables, context_lens, q_start, out, out_dtype, lse_out,
+                                      want_lse)
+    _shape(w_uk, (q.shape[1], dn, r), "w_uk")
+    _shape(w_uv, (q.shape[1], dv, r), "w_uv")
+    with _same_device(q, latent_cache, w_uk, w_uv, block_tables, context_lens, workspace, q_start, out, lse_out):
+        _check(_lib.kf_latent_attention_expanded(
+            _dev(q, torch.bfloat16, "q"), _opt(q_start, torch.int32, "q_start"),
+            _dev(latent_cache, torch.bfloat16, "latent_cache"), _dev(w_uk, torch.bfloat16, "w_uk"),
+            _dev(w_uv, torch.bfloat16, "w_uv"), _dev(block_tables, torch.int32, "block_tables"),
+            block_tables.shape[1], _dev(context_lens, torch.int32, "context_lens"), int(bool(causal)),
+            int(max_context_len), int(max_query_len), block_tables.shape[0], q.shape[0], q.shape[1], r, rope, dn, dv,
+            bs, nb, float(scale), _dev(workspace, torch.uint8, "workspace"), workspace.numel(),
+            _dev(out, out.dtype, "out"), code, _opt(lse_out, torch.float32, "lse_out"), _stream(stream)),
+            "kf_latent_attention_expanded")
+    return out, lse_out
+
+
+def _accumulate(name, q, k_cache, k_scale, block_tables, context_lens, max_context_len, scale, lse, scores_out,
+                scores_in, q_start, max_query_len, causal, stream):
+    nq, hq, d = q.shape
+    nb, bs, hkv, _ = k_cache.shape
+    _shape(k_cache, (nb, bs, hkv, d), "k_cache")
+    B = block_tables.shape[0]
+    _shape(context_lens, (B,), "context_lens")
+    _shape(lse, (nq, hq), "lse")
+    if scores_out.dim() != 2 or scores_out.shape[0] != B:
+        raise ValueError("scores_out must be [batch, stride]")
+    if scores_in is not None:
+        _shape(scores_in, scores_out.shape, "scores_in")
+    if q_start is not None:
+        _shape(q_start, (B + 1,), "q_start")
+    elif nq != B:
+        raise ValueError("q must hold one query token a request without q_start")
+    if k_scale is not None:
+        _shape(k_scale, (hkv,), "k_scale")
+    cache = _dev(k_cache, torch.bfloat16, "k_cache") if k_scale is None else _dev8(k_cache, "k_cache")
+    with _same_device(q, k_cache, k_scale, block_tables, context_lens, lse, scores_out, scores_in, q_start):
+        scales = () if k_scale is None else (_dev(k_scale, torch.float32, "k_scale"),)
+        _check(getattr(_lib, name)(
+            _dev(q, torch.bfloat16, "q"), _opt(q_start, torch.int32, "q_start"), cache, *scales,
+            _dev(block_tables, torch.int32, "block_tables"), block_tables.shape[1],
+            _dev(context_lens, torch.int32, "context_lens"), int(bool(causal)), int(max_context_len),
+            int(max_query_len), B, nq, hq, hkv, d, bs, nb, float(scale), _dev(lse, torch.float32, "lse"),
+            _opt(scores_in, torch.float32, "scores_in"), _dev(scores_out, torch.float32, "scores_out"),
+            scores_out.shape[1], _stream(stream)), name)
+    return scores_out
+
+
+def kf_accumulate_attention(q: torch.Tensor, k_cache: torch.Tensor, block_tables: torch.Tensor,
+                            context_lens: torch.Tensor, max_context_len: int, scale: float, lse: torch.Tensor,
+                            scores_out: torch.Tensor, scores_in: Optional[torch.Tensor] = None,
+                            q_start: Optional[torch.Tensor] = None, max_query_len: int = 1, causal: bool = True,
+                            stream=None) -> torch.Tensor:
+    """scores_out[b, t] = scores_in[b, t] + the attention weight token t receives
+    from the queries q [Nq, Hq, D] whose log-sum-exp is lse [Nq, Hq]; scores_out
+    [B, stride] may be scores_in (None: zeros). Returns scores_out."""
+    return _accumulate("kf_accumulate_attention", q, k_cache, None, block_tables, context_lens, max_context_len,
+                       scale, lse, scores_out, scores_in, q_start, max_query_len, causal, stream)
+
+
+def kf_accumulate_attention_fp8(q, k_cache, k_scale, block_tables, context_lens, max_context_len: int,
+                                scale: float, lse, scores_out, scores_in=None, q_start=None, max_query_len: int = 1,
+                                causal: bool = True, stream=None) -> torch.Tensor:
+    """kf_accumulate_attention over an E4M3 key cache."""
+    return _accumulate("kf_accumulate_attention_fp8", q, k_cache, k_scale, block_tables, context_lens,
+                       max_context_len, scale, lse, scores_out, scores_in, q_start, max_query_len, causal, stream)
+
+
+def kf_evict_workspace_size(batch: int, max_context_len: int, keep: int) -> int:
+    return int(_lib.kf_evict_workspace_size(batch, max_context_len, keep))
+
+
+def make_evict_workspace(batch: int, max_context_len: int, keep: int, device=None) -> torch.Tensor:
+    """A workspace for kf_evict_tokens (any contents)."""
+    n = kf_evict_workspace_size(batch, max_context_len, keep)
+    return torch.empty(max(n, 16), dtype=torch.uint8, device=device or "cuda")
+
+
+def kf_evict_tokens(caches, block_tables: torch.Tensor, context_lens: torch.Tensor, max_context_len: int,
+                    scores: torch.Tensor, keep: int, sink: int, recent: int, context_lens_out: torch.Tensor,
+                    scores_out: torch.Tensor, workspace: torch.Tensor, positions: Optional[torch.Tensor] = None,
+                    seq_lens: Optional[torch.Tensor] = None, positions_out: Optional[torch.Tensor] = None,
+                    stream=None) -> None:
+    """Cut every request to its `keep` tokens of most weight, in place. caches: one
+    or two paged caches ([num_blocks, block_size, ...], rows of equal bytes: K and
+    V, or a latent cache). The *_out tensors may be their inputs."""
+    caches = list(caches)
+    if len(caches) not in (1, 2):
+        raise ValueError("caches must be one or two tensors")
+    first = caches[0]
+    for c in caches:
+        if c.dim() < 3 or c.shape != first.shape or c.dtype != first.dtype:
+            raise ValueError("caches must share one [num_blocks, block_size, ...] shape and type")
+    nb, bs = first.shape[:2]
+    row_bytes = first[0, 0].numel() * first.element_size() if nb and bs else 0
+    B = block_tables.shape[0]
+    for t, n in ((context_lens, "context_lens"), (context_lens_out, "context_lens_out"), (seq_lens, "seq_lens")):
+        if t is not None:
+            _shape(t, (B,), n)
+    if scores.dim() != 2 or scores.shape[0] != B:
+        raise ValueError("scores must be [batch, stride]")
+    for t, n in ((scores_out, "scores_out"), (positions, "positions"), (positions_out, "positions_out")):
+        if t is not None:
+            _shape(t, scores.shape, n)
+    with _same_device(*caches, block_tables, context_lens, scores, context_lens_out, scores_out, workspace, positions,
+                      seq_lens, positions_out):
+        ptr = [_dev(c, c.dtype, "caches") for c in caches] + [None]
+        _check(_lib.kf_evict_tokens(
+            ptr[0], ptr[1], row_bytes, _dev(block_tables, torch.int32, "block_tables"), block_tables.shape[1],
+            _dev(context_lens, torch.int32, "context_lens"), int(max_context_len), B, bs, nb,
+            _dev(scores, torch.float32, "scores"), _dev(scores_out, torch.float32, "scores_out"), scores.shape[1],
+            _opt(positions, torch.int32, "positions"), _opt(positions_out, torch.int32, "positions_out"),
+            _opt(seq_lens, torch.int32, "seq_lens"), int(keep), int(sink), int(recent),
+            _dev(context_lens_out, torch.int32, "context_lens_out"), _dev(workspace, torch.uint8, "workspace"),
+            workspace.numel(), _stream(stream)), "kf_evict_tokens")
 
 
 def kf_check_bounded_wait(stream=None) -> None:
