@@ -186,21 +186,6 @@ expand_simple_kernel(const LatentParams p, const uint16_t *__restrict__ w, T *__
 
 }  // namespace
 
-size_t latent_workspace_bytes(int batch, int max_query_len, int num_heads, int latent_dim, int sm_count) {
-    return 256;
-}
-
-cudaError_t launch_latent(const LatentParams &p, void *workspace, int sm_count, cudaStream_t stream, void *encode_fn) {
-    const int64_t tiles = ((int64_t)p.max_query_len * p.num_heads + kRows - 1) / kRows;
-    const int KS = p.latent_dim + kRopeDim + 1;
-    const size_t smem = (size_t)(kRows * KS + kTok * KS + kRows * kTok + 3 * kRows) * 4;
-    cudaError_t e = cudaFuncSetAttribute(latent_simple_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         (int)smem);
-    if (e != cudaSuccess) return e;
-    latent_simple_kernel<false><<<dim3((unsigned)tiles, p.batch), kThreads, smem, stream>>>(p, ExpandedKV{});
-    return cudaGetLastError();
-}
-
 size_t latent_expanded_workspace_bytes(int batch, int num_q_tokens, int max_context_len, int num_heads, int nope,
                                        int v) {
     const size_t cap = ((size_t)max_context_len + 127) / 128 * 128;

@@ -1,0 +1,819 @@
+// kf_latent_tc05.cu -- latent attention, absorbed form, on tcgen05.
+//
+// Query rows (query token j, head h) of a request share every key: row r of the
+// request is q[q_start + r / H, r % H], contiguous in memory. With the latent
+// row x_t = [c_t ; r_t] of R + 64 numbers,
+//   S = Q X^T  (K = R + 64),   P = softmax rows,   O = P C  (C = the first R columns of X),
+// so one tile of X in shared memory serves both products: keys as they are, values
+// as the same bytes read along the other axis.
+//
+// Work. Rows come in tiles of 64, tokens in tiles of 64. A unit is one row tile of
+// one request over all its token tiles; the units of the batch, laid end to end,
+// are cut into equal runs, one a CTA (one CTA an SM: the tile ring fills its
+// shared memory). A run may start and end inside a unit; the parts of such a unit
+// go to the workspace as normalised (o, lse) partials and latent_merge joins
+// them. So a batch of any length mix keeps every SM busy to the end, at the
+// price of at most two partials a CTA.
+//
+// One tile: 64 x (R + 64) bf16 arrive as one TMA box a cache block, landing as
+// 8-token groups of 128-byte-swizzled atoms (group, 64-column atom, token, column).
+//   S[64 rows x 64 tokens]     = Q X^T          A = Q, B = X, both K-major, M = 64
+//   O^T[128 columns x rows]   += C^T P^T        A = C^T (M-major: the same tile), B = P
+// The value product is taken transposed, R / 128 instructions of M = 128 and N = the
+// rows in use (rounded up to 16): its accumulator then takes R / 128 * 64 TMEM
+// columns instead of R, which leaves room for two score tiles, and its work
+// shrinks with the rows. P goes through shared memory as that product's B.
+//   warps 0-3  softmax: rows 16 w .. 16 w + 15, four lanes a row (16x256b TMEM loads:
+//              lane l holds columns 8 i + 2 (l % 4), + 1 of rows l / 4 and l / 4 + 8);
+//              base-2 online softmax with a lazy maximum (it moves only by more
+//              than 8, and then O^T's columns are rescaled in TMEM); the epilogue.
+//   warp 4     TMA producer;  warp 5  issues S and owns TMEM;  warp 6  issues O^T.
+// Score tiles alternate between two TMEM buffers, and the two products have an issuing
+// warp each: S of tile g + 1 goes out as soon as its tile has landed, the value
+// product of tile g as soon as its weights are there, whichever comes first.
+//
+// What bounds it: 2 (R + 64) bytes of cache a token. At R = 512 an SM's share of HBM
+// brings a token in 53 cycles (64 tokens x 1152 B at 44.6 B/ns); the instructions
+// take 26 (M = 64 runs at half rate) and shared memory 40 (fill, Q and X for S, C
+// and P for O), so up to 64 rows the cache is the bound; each further 64 rows
+// read the tile again, from L2.
+//
+// Tokens past a unit's last visible one are masked by selection (never multiplied)
+// and their rows zeroed in shared memory (0 * NaN would poison the product).
+// Every wait is bounded; one that gives up sets KF_DEVERR_TIMEOUT and the CTA
+// drains its copies and MMAs, frees its TMEM and returns.
+#include "kf_latent.cuh"
+#include "kf_mq_tc05.cuh"
+
+#include <algorithm>
+
+namespace kf {
+namespace {
+
+using namespace tc;
+using namespace mq5;
+
+constexpr int kM = 64;   // rows a unit
+constexpr int kN = 64;   // tokens a tile
+constexpr int kSoftThreads = 128, kProducerWarp = 4, kScoreWarp = 5, kValueWarp = 6, kThreads = 224;
+
+template <int R>
+struct LShape {
+    static constexpr int kAtoms = (R + kRopeDim) / 64;
+    static constexpr int kGroupBytes = kAtoms * 1024;         // 8 tokens
+    static constexpr int kTileBytes = kN / 8 * kGroupBytes;
+    static constexpr int kQAtomBytes = kM * 128;              // 64 rows x 64 columns
+    static constexpr int kQBytes = kAtoms * kQAtomBytes;
+    static constexpr int kPBytes = kM * kN * 2;
+    static constexpr int kStages = R == 512 ? 2 : 4;
+    static constexpr int kSmemBytes = kQBytes + kStages * kTileBytes + kPBytes + 1024;
+    static constexpr int kDimTiles = R / 128;
+    static constexpr uint32_t kColS = 256;                    // two score tiles; O^T below
+    static_assert(kSmemBytes > 116 * 1024 && kSmemBytes <= 225 * 1024, "one CTA an SM");
+    static_assert(kDimTiles * 64 <= 256, "O^T columns");
+};
+
+// ---------------------------------------------------------------------------
+// The schedule: units of a request and the run of each CTA.
+// ---------------------------------------------------------------------------
+struct Request {
+    int64_t q0, rows, L, shift;  // query j sees tokens [0, min(shift + j + 1, L))
+    int64_t n;                   // token tiles charged to each unit (at least one)
+    int units;
+};
+
+__device__ __forceinline__ Request request_of(const LatentParams &p, int b, bool report) {
+    const LatentRequest r = latent_request(p, b, report);
+    if (r.q0 < 0) return {0, 0, 0, 0, 1, 0};
+    const int64_t C = r.C < p.max_query_len ? r.C : p.max_query_len;
+    Request q;
+    q.q0 = r.q0;
+    q.rows = C * p.num_heads;
+    q.L = r.L < p.max_context_len ? r.L : p.max_context_len;
+    q.shift = r.L - r.C;
+    q.n = q.L > 0 ? (q.L + kN - 1) / kN : 1;
+    q.units = (int)((q.rows + kM - 1) / kM);
+    return q;
+}
+
+// The first tile of CTA i's run when T tiles are cut into min(ctas, T) equal runs
+// (CTAs past the last run have none).
+__device__ __forceinline__ int64_t cut_at(int i, int ctas, int64_t T) {
+    const int64_t P = ctas < T ? ctas : T;
+    return i < P ? i * T / P : T;
+}
+
+struct Place {
+    int b;
+    int64_t off;  // tiles into the request
+};
+
+// Where the batch's tile `slot_of(T)` lies, and T. All threads of the block (whole
+// warps, at most 1024) call it; `sm` holds 36 int64.
+template <typename F>
+__device__ __forceinline__ int64_t locate(const LatentParams &p, bool report, int64_t *sm, F slot_of, Place &place,
+                                          int64_t &slot) {
+    const int tid = threadIdx.x, nt = blockDim.x, lane = tid & 31, warp = tid >> 5;
+    const int per = (p.batch + nt - 1) / nt;
+    const int b0 = min(tid * per, p.batch), b1 = min(b0 + per, p.batch);
+    int64_t mine = 0;
+    for (int b = b0; b < b1; ++b) {
+        const Request r = request_of(p, b, report);
+        mine += r.n * r.units;
+    }
+    int64_t v = mine;
+    for (int o = 1; o < 32; o <<= 1) {
+        const int64_t y = __shfl_up_sync(0xffffffffu, v, o);
+        if (lane >= o) v += y;
+    }
+    if (lane == 31) sm[warp] = v;
+    __syncthreads();
+    int64_t before = v - mine, total = 0;
+    for (int w = 0; w < nt / 32; ++w) {
+        if (w < warp) before += sm[w];
+        total += sm[w];
+    }
+    slot = slot_of(total);
+    if (slot >= before && slot < before + mine) {
+        int64_t at = before;
+        for (int b = b0; b < b1; ++b) {
+            const Request r = request_of(p, b, false);
+            if (slot < at + r.n * r.units) {
+                sm[34] = b;
+                sm[35] = slot - at;
+                break;
+            }
+            at += r.n * r.units;
+        }
+    }
+    __syncthreads();
+    place.b = (int)sm[34];
+    place.off = sm[35];
+    return total;
+}
+
+// One unit's part in a CTA's run: token tiles [tile0, tile0 + tiles).
+struct Segment {
+    int64_t q0, row0, L, shift;
+    int rows, tile0, tiles;
+    int t_end;          // the last token any row of the unit sees, plus one
+    int b;
+    bool whole, first;  // the unit lies in this run alone; it is the run's first segment
+};
+
+struct Walker {
+    Place at;
+    int64_t left;
+    bool first = true;
+    Request r;
+    bool loaded = false;
+
+    __device__ __forceinline__ bool next(const LatentParams &p, Segment &s) {
+        while (left > 0) {
+            if (!loaded) {
+                r = request_of(p, at.b, false);
+                loaded = true;
+            }
+            if (at.off >= r.n * r.units) {  // on to the next request (some have no units)
+                ++at.b;
+                at.off = 0;
+                loaded = false;
+                if (at.b >= p.batch) return false;
+                continue;
+            }
+            const int64_t unit = at.off / r.n, tile = at.off - unit * r.n;
+            const int64_t len = left < r.n - tile ? left : r.n - tile;
+            s.q0 = r.q0;
+            s.row0 = unit * kM;
+            s.rows = (int)(r.rows - s.row0 < kM ? r.rows - s.row0 : kM);
+            s.L = r.L;
+            s.shift = r.shift;
+            s.b = at.b;
+            s.whole = len == r.n;
+            s.first = first;
+            int64_t end = r.L;
+            if (p.causal) {
+                const int64_t lim = r.shift + (s.row0 + s.rows - 1) / p.num_heads + 1;
+                if (lim < end) end = lim < 0 ? 0 : lim;
+            }
+            s.t_end = (int)end;
+            const int64_t valid = (end + kN - 1) / kN;  // tiles any row sees
+            const int64_t hi = tile + len < valid ? tile + len : valid;
+            s.tile0 = (int)tile;
+            s.tiles = hi > tile ? (int)(hi - tile) : 0;
+            at.off += len;
+            left -= len;
+            first = false;
+            return true;
+        }
+        return false;
+    }
+};
+
+struct Partials {
+    float *o;    // [2 * CTAs][row pitch][R]
+    float *lse;  // [2 * CTAs][row pitch]
+    int pitch;   // rows a slot holds
+};
+
+// ---------------------------------------------------------------------------
+// PTX
+// ---------------------------------------------------------------------------
+// 16 lanes x 64 columns: lane l gets columns 8 i + 2 (l % 4) + {0, 1} of TMEM lanes
+// l / 4 (r[4 i], r[4 i + 1]) and l / 4 + 8 (r[4 i + 2], r[4 i + 3]), waited for.
+__device__ __forceinline__ void tmem_ld_16x256b_x8(uint32_t taddr, uint32_t (&r)[32]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.16x256b.x8.b32 {"
+        "%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31"
+        "}, [%32];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
+          "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
+          "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(taddr)
+        : "memory");
+}
+
+// Columns [col, col + 16) of this thread's TMEM lane, waited for.
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {"
+        "%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15"
+        "}, [%16];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr)
+        : "memory");
+}
+
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap *map, int x, int y, int z, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(bar)
+        : "memory");
+}
+
+// One lane of a converged warp (the same one every time).
+__device__ __forceinline__ bool elect_one() {
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+    return r != 0;
+}
+
+// The softmax warps' barrier, and the same with an OR of one predicate.
+__device__ __forceinline__ void soft_sync() { asm volatile("barrier.cta.sync 1, 128;" ::: "memory"); }
+
+__device__ __forceinline__ bool soft_any(bool x) {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %1, 0;\n\t"
+        "barrier.cta.red.or.pred q, 1, 128, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(r)
+        : "r"((uint32_t)x)
+        : "memory");
+    return r != 0;
+}
+
+// ---------------------------------------------------------------------------
+// Attention
+// ---------------------------------------------------------------------------
+template <int R>
+__global__ void __launch_bounds__(kThreads, 1)
+latent_kernel(const LatentParams p, const Partials part, const __grid_constant__ CUtensorMap tmap_x,
+              const __grid_constant__ CUtensorMap tmap_q) {
+    using Sh = LShape<R>;
+    constexpr int NS = Sh::kStages, KS = (R + kRopeDim) / 16, KP = kN / 16;
+    // full[NS], empty[NS], q_full, q_empty, s_full[2], s_empty[2], p_full, pv_done, o_empty, fin[2]
+    __shared__ __align__(8) uint64_t bar_mem[2 * NS + 11];
+    __shared__ int64_t sm_loc[36];
+    __shared__ float sm_alpha[kM], sm_lse[kM];
+    __shared__ uint32_t tmem_slot;
+    __shared__ volatile int abort_flag;
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
+    const uint32_t sQ = base, sX = base + Sh::kQBytes, sP = sX + NS * Sh::kTileBytes;
+    const uint32_t bars = smem_u32(bar_mem);
+    auto full = [&](int i) { return bars + 8u * i; };
+    auto empty = [&](int i) { return bars + 8u * (NS + i); };
+    const uint32_t q_full = bars + 8u * (2 * NS), q_empty = q_full + 8;
+    auto s_full = [&](uint32_t i) { return q_full + 16 + 8 * i; };
+    auto s_empty = [&](uint32_t i) { return q_full + 32 + 8 * i; };
+    const uint32_t p_full = q_full + 48, pv_done = q_full + 56, o_empty = q_full + 64, fin = q_full + 72;
+    const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < NS; ++i) {
+            mbar_init(full(i), 1);
+            mbar_init(empty(i), 1);
+        }
+        mbar_init(q_full, 1);
+        mbar_init(q_empty, 1);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(s_full(i), 1);
+            mbar_init(s_empty(i), kSoftThreads);
+        }
+        mbar_init(p_full, kSoftThreads);
+        mbar_init(pv_done, 1);
+        mbar_init(o_empty, kSoftThreads);
+        mbar_init(fin, 1);
+        mbar_init(fin + 8, 1);
+        abort_flag = (*(volatile unsigned int *)p.err & KF_DEVERR_TIMEOUT) ? 1 : 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == kProducerWarp && lane == 0) {
+        asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tmap_x)) : "memory");
+        asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tmap_q)) : "memory");
+    }
+    if (warp == kScoreWarp) tc05::tmem_alloc(smem_u32(&tmem_slot), 512);
+    Walker walk;
+    int64_t slot0;
+    const int64_t total = locate(
+        p, blockIdx.x == 0, sm_loc, [&](int64_t T) { return cut_at(blockIdx.x, gridDim.x, T); }, walk.at, slot0);
+    walk.left = cut_at(blockIdx.x + 1, gridDim.x, total) - slot0;
+    if (abort_flag) walk.left = 0;  // an earlier kernel's wait gave up (no role has started yet)
+    tc05::fence_before_sync();
+    __syncthreads();
+    tc05::fence_after_sync();
+    const uint32_t tm = tmem_slot;
+    const int bs_shift = block_shift(p.block_size);
+    // an issuing warp's end: report a wait that gave up, and see every MMA issued done
+    // before TMEM is freed
+    auto finish = [&](bool ok, uint32_t bar) {
+        if (elect_one()) {
+            if (!ok) {
+                raise_error(p.err, KF_DEVERR_TIMEOUT);
+                abort_flag = 1;
+            }
+            tc05::commit(bar);
+            if (!mbar_wait(bar, 0)) raise_error(p.err, KF_DEVERR_TIMEOUT);
+        }
+        __syncwarp();
+    };
+
+    if (warp == kProducerWarp) {
+        // ------------------------------ producer ------------------------------
+        const uint32_t box_bytes = (uint32_t)p.block_size * (R + kRopeDim) * 2;
+        const int max_blk = kN >> bs_shift;
+        uint32_t g = 0, nseg = 0, q_loads = 0;
+        bool ok = true;
+        Segment s;
+        while (ok && walk.next(p, s)) {
+            if (s.tiles == 0) continue;
+            for (int i = 0; i < s.tiles; ++i, ++g) {
+                const int t0 = (s.tile0 + i) * kN;
+                const int ntok = s.t_end - t0 < kN ? s.t_end - t0 : kN;
+                const int nblk = (ntok + p.block_size - 1) >> bs_shift;
+                // this tile's table entries, asked for before the wait for its slot
+                int64_t phys = 0;
+                if (lane < max_blk && lane < nblk) {
+                    const int64_t e = (t0 >> bs_shift) + lane;
+                    phys = e < p.bt_stride ? p.block_tables[(int64_t)s.b * p.bt_stride + e] : -1;
+                    if (phys < 0 || phys >= p.num_blocks) {
+                        raise_error(p.err, KF_DEVERR_BLOCK_ID);
+                        phys = 0;
+                    }
+                }
+                const uint32_t st = g % NS;
+                int go = 1;
+                if (lane == 0) {
+                    go = !abort_flag && mbar_wait(empty(st), ((g / NS) & 1) ^ 1);
+                    if (go && i == 0) {
+                        go = mbar_wait(q_empty, (nseg & 1) ^ 1);
+                        if (go) {
+                            ++q_loads;
+                            mbar_arrive_expect_tx(q_full, Sh::kQBytes);
+                            tma_load_3d(sQ, &tmap_q, 0, (int)(s.q0 * p.num_heads + s.row0), 0, q_full);
+                        }
+                    }
+                    if (go) mbar_arrive_expect_tx(full(st), nblk * box_bytes);
+                    else {
+                        raise_error(p.err, KF_DEVERR_TIMEOUT);
+                        abort_flag = 1;
+                    }
+                }
+                ok = __shfl_sync(0xffffffffu, go, 0);
+                if (!ok) break;
+                if (lane < nblk)
+                    tma_load_4d(sX + st * Sh::kTileBytes + lane * box_bytes, &tmap_x, 0, 0, 0,
+                                (int)(phys * (p.block_size / 8)), full(st));
+                __syncwarp();
+            }
+            ++nseg;
+        }
+        if (lane == 0) {
+            // drain: the last use of every slot has landed before the CTA can exit
+            for (uint32_t j = g > NS ? g - NS : 0; j < g; ++j)
+                if (!mbar_wait(full(j % NS), (j / NS) & 1)) raise_error(p.err, KF_DEVERR_TIMEOUT);
+            if (q_loads > 0 && !mbar_wait(q_full, (q_loads - 1) & 1)) raise_error(p.err, KF_DEVERR_TIMEOUT);
+        }
+    } else if (warp == kScoreWarp) {
+        // ----------------------------- score issuer -----------------------------
+        // (whole warps walk and wait, one elected lane issues: the descriptors then
+        // stay in uniform registers, 36 cycles an instruction instead of 58)
+        const uint32_t id_s = tc05::idesc_bf16(kM, kN, false, false);
+        const uint64_t qd = tc05::sdesc_sw128(sQ, 16, 1024);
+        uint32_t g = 0, nseg = 0;
+        bool ok = true;
+        Segment s;
+        while (ok && walk.next(p, s)) {
+            const int tiles = __shfl_sync(0xffffffffu, s.tiles, 0);
+            if (tiles == 0) continue;
+            ok = warp_wait(q_full, nseg & 1);
+            for (int i = 0; i < tiles && ok; ++i, ++g) {
+                const uint32_t st = g % NS, sb = g & 1;
+                ok = !__any_sync(0xffffffffu, abort_flag) && warp_wait(full(st), (g / NS) & 1) &&
+                     warp_wait(s_empty(sb), ((g >> 1) & 1) ^ 1);
+                if (!ok) break;
+                tc05::fence_after_sync();
+                const uint64_t xd = tc05::sdesc_sw128(sX + st * Sh::kTileBytes, 16, Sh::kGroupBytes);
+                if (elect_one()) {
+#pragma unroll
+                    for (int kk = 0; kk < KS; ++kk)
+                        tc05::mma_ss(tm + Sh::kColS + 64 * sb,
+                                     qd + (uint64_t)(((kk >> 2) * Sh::kQAtomBytes + 32 * (kk & 3)) / 16),
+                                     xd + (uint64_t)(((kk >> 2) * 1024 + 32 * (kk & 3)) / 16), id_s, kk > 0 ? 1u : 0u);
+                    tc05::commit(s_full(sb));
+                    if (i == tiles - 1) tc05::commit(q_empty);
+                }
+                __syncwarp();
+            }
+            ++nseg;
+        }
+        finish(ok, fin);
+    } else if (warp == kValueWarp) {
+        // ----------------------------- value issuer -----------------------------
+        const uint64_t pd = tc05::sdesc_sw128(sP, 16, 1024);
+        uint32_t g = 0, nseg = 0;
+        bool ok = true;
+        Segment s;
+        while (ok && walk.next(p, s)) {
+            const int tiles = __shfl_sync(0xffffffffu, s.tiles, 0);
+            if (tiles == 0) continue;
+            const uint32_t id_o =
+                tc05::idesc_bf16(128, __shfl_sync(0xffffffffu, (s.rows + 15) / 16 * 16, 0), true, false);
+            // the previous segment's O^T has been read out
+            ok = warp_wait(o_empty, (nseg & 1) ^ 1);
+            for (int i = 0; i < tiles && ok; ++i, ++g) {
+                const uint32_t st = g % NS;
+                ok = !__any_sync(0xffffffffu, abort_flag) && warp_wait(p_full, g & 1);
+                if (!ok) break;
+                tc05::fence_after_sync();
+                const uint64_t cd = tc05::sdesc_sw128(sX + st * Sh::kTileBytes, 1024, Sh::kGroupBytes);
+                if (elect_one()) {
+#pragma unroll
+                    for (int d = 0; d < Sh::kDimTiles; ++d)
+#pragma unroll
+                        for (int kk = 0; kk < KP; ++kk)
+                            tc05::mma_ss(tm + 64 * d, cd + (uint64_t)((d * 2048 + kk * 2 * Sh::kGroupBytes) / 16),
+                                         pd + (uint64_t)(32 * kk / 16), id_o, (i > 0 || kk > 0) ? 1u : 0u);
+                    tc05::commit(empty(st));
+                    tc05::commit(pv_done);
+                }
+                __syncwarp();
+            }
+            ++nseg;
+        }
+        finish(ok, fin + 8);
+    } else {
+        // ------------------------------- softmax --------------------------------
+        const uint32_t lane_base = (uint32_t)(32 * warp) << 16;
+        const float c = p.scale_log2;
+        const int rr[2] = {16 * warp + (lane >> 2), 16 * warp + (lane >> 2) + 8};  // this lane's rows
+        uint32_t g = 0;
+        bool fail = false, stop = false;  // fail: this warp's wait gave up; stop: all four warps leave
+        Segment s;
+        while (!stop && walk.next(p, s)) {
+            float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+            int lim[2];  // tokens these rows see (none: rows past the unit's last)
+            for (int k = 0; k < 2; ++k) {
+                int64_t x = s.t_end;
+                if (p.causal && s.shift + (s.row0 + rr[k]) / p.num_heads + 1 < x)
+                    x = s.shift + (s.row0 + rr[k]) / p.num_heads + 1;
+                lim[k] = rr[k] < s.rows && x > 0 ? (int)x : 0;
+            }
+            for (int i = 0; i < s.tiles; ++i, ++g) {
+                const int t0 = (s.tile0 + i) * kN;
+                const uint32_t sb = g & 1;
+                if (!warp_wait(s_full(sb), (g >> 1) & 1)) fail = true;
+                tc05::fence_after_sync();
+                uint32_t x[32];
+                tmem_ld_16x256b_x8(tm + lane_base + Sh::kColS + 64 * sb, x);
+                tc05::fence_before_sync();
+                mbar_arrive(s_empty(sb));
+                // tokens past the last visible one: their rows become zeros
+                const int ntok = s.t_end - t0;
+                if (ntok < kN) {
+                    const uint32_t xt = sX + (g % NS) * Sh::kTileBytes;
+                    constexpr int CH = R / 8;  // 16-byte chunks of a value row
+                    for (int k = threadIdx.x; k < (kN - ntok) * CH; k += kSoftThreads) {
+                        const int t = ntok + k / CH, ch = k % CH;
+                        asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(
+                                         xt + (t >> 3) * Sh::kGroupBytes + (ch >> 3) * 1024 + (t & 7) * 128 +
+                                         (ch & 7) * 16),
+                                     "r"(0u)
+                                     : "memory");
+                    }
+                }
+                float mx[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+#pragma unroll
+                    for (int k = 0; k < 2; ++k)
+#pragma unroll
+                        for (int u = 0; u < 2; ++u) {
+                            const int t = t0 + 8 * e + 2 * (lane & 3) + u;
+                            const float v = t < lim[k] ? __uint_as_float(x[4 * e + 2 * k + u]) * c : -INFINITY;
+                            x[4 * e + 2 * k + u] = __float_as_uint(v);
+                            mx[k] = fmaxf(mx[k], v);
+                        }
+                bool need = false;
+                float alpha[2];
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    mx[k] = fmaxf(mx[k], __shfl_xor_sync(0xffffffffu, mx[k], 1));
+                    mx[k] = fmaxf(mx[k], __shfl_xor_sync(0xffffffffu, mx[k], 2));
+                    const bool up = mx[k] > m[k] + kRescaleSlack;
+                    alpha[k] = up ? exp2f(m[k] - mx[k]) : 1.f;  // m = -inf: 0
+                    if (up) {
+                        l[k] *= alpha[k];
+                        m[k] = mx[k];
+                        need = need || i > 0;
+                    }
+                }
+                // one barrier a tile in the common case; O^T is rescaled (and a wait that
+                // gave up acted on) by all four warps together
+                const bool any = soft_any(need || fail);
+                // the P buffer is free, and O^T complete, once the previous value product is done
+                if (g > 0 && !warp_wait(pv_done, (g - 1) & 1)) fail = true;
+                if (any) {
+                    stop = soft_any(fail);
+                    if (stop) break;
+                    if ((lane & 3) == 0) {
+                        sm_alpha[rr[0]] = alpha[0];
+                        sm_alpha[rr[1]] = alpha[1];
+                    }
+                    soft_sync();
+                    tc05::fence_after_sync();
+                    for (int d = 0; d < Sh::kDimTiles; ++d)
+                        for (int q = 0; q < (s.rows + 15) / 16; ++q) {
+                            uint32_t o[16];
+                            tmem_ld16(tm + lane_base + 64 * d + 16 * q, o);
+#pragma unroll
+                            for (int e = 0; e < 16; ++e)
+                                o[e] = __float_as_uint(__uint_as_float(o[e]) * sm_alpha[16 * q + e]);
+                            tc05::tmem_st16(tm + lane_base + 64 * d + 16 * q, o);
+                        }
+                }
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    const float mu = m[k] == -INFINITY ? 0.f : m[k];
+                    const uint32_t row = sP + rr[k] * 128;
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        const float a = ex2f(__uint_as_float(x[4 * e + 2 * k]) - mu);
+                        const float b = ex2f(__uint_as_float(x[4 * e + 2 * k + 1]) - mu);
+                        l[k] += a + b;
+                        asm volatile("st.shared.u32 [%0], %1;" ::"r"(row + ((e ^ (rr[k] & 7)) << 4) + (lane & 3) * 4),
+                                     "r"(pack_bf16(a, b))
+                                     : "memory");
+                    }
+                }
+                fence_proxy_async_smem();
+                tc05::fence_before_sync();
+                mbar_arrive(p_full);
+            }
+            if (stop) break;
+            // epilogue: row sums over the four lanes of a row, then O^T column by column
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                l[k] += __shfl_xor_sync(0xffffffffu, l[k], 1);
+                l[k] += __shfl_xor_sync(0xffffffffu, l[k], 2);
+                if ((lane & 3) == 0) {
+                    sm_alpha[rr[k]] = l[k] > 0.f ? 1.f / l[k] : 0.f;
+                    sm_lse[rr[k]] = l[k] > 0.f ? (m[k] + log2f(l[k])) * 0.6931471805599453f : -INFINITY;
+                }
+            }
+            if (s.tiles > 0 && !warp_wait(pv_done, (g - 1) & 1)) fail = true;
+            stop = soft_any(fail);
+            if (stop) break;
+            const int64_t slot = 2 * (int64_t)blockIdx.x + (s.first ? 0 : 1);
+            const int64_t row_out = s.q0 * p.num_heads + s.row0;
+            if (s.tiles > 0) tc05::fence_after_sync();
+            for (int d = 0; d < Sh::kDimTiles; ++d) {
+                const int dim = 128 * d + threadIdx.x;
+                for (int q = 0; q < (s.rows + 15) / 16; ++q) {
+                    uint32_t o[16];
+                    if (s.tiles > 0) tmem_ld16(tm + lane_base + 64 * d + 16 * q, o);
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) {
+                        const int r = 16 * q + e;
+                        const float inv = sm_alpha[r];
+                        const float v = s.tiles > 0 && inv > 0.f ? __uint_as_float(o[e]) * inv : 0.f;
+                        if (r >= s.rows) continue;
+                        if (!s.whole) part.o[(slot * part.pitch + r) * R + dim] = v;
+                        else if (p.out_dtype == KF_F32) static_cast<float *>(p.out)[(row_out + r) * R + dim] = v;
+                        else static_cast<__nv_bfloat16 *>(p.out)[(row_out + r) * R + dim] = __float2bfloat16(v);
+                    }
+                }
+            }
+            if (threadIdx.x < s.rows) {
+                if (!s.whole) part.lse[slot * part.pitch + threadIdx.x] = sm_lse[threadIdx.x];
+                else if (p.lse_out) p.lse_out[row_out + threadIdx.x] = sm_lse[threadIdx.x];
+            }
+            tc05::fence_before_sync();
+            if (s.tiles > 0) mbar_arrive(o_empty);
+            soft_sync();  // sm_alpha and sm_lse are free again
+        }
+        if (stop) {
+            if (threadIdx.x == 0) raise_error(p.err, KF_DEVERR_TIMEOUT);
+            abort_flag = 1;
+        }
+    }
+    tc05::fence_before_sync();
+    __syncthreads();
+    if (warp == kScoreWarp) {
+        tc05::fence_after_sync();
+        tc05::tmem_dealloc(tm, 512);
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Merge of the units that more than one CTA worked on. Block x handles the unit
+// cut at the start of CTA x + 1's run, if that is the unit's first cut; RPB rows
+// a block, 8 / RPB warps a row, each over every (8 / RPB)-th partial:
+//   M = max lse_i, w_i = e^{lse_i - M}, out = sum w_i o_i / sum w_i.
+// ---------------------------------------------------------------------------
+template <int R, int RPB>
+__global__ void __launch_bounds__(256)
+latent_merge_kernel(const LatentParams p, const Partials part, int ctas) {
+    constexpr int WPR = 8 / RPB, V = R / 128;  // warps a row; float4 a lane
+    __shared__ int64_t sm_loc[36];
+    __shared__ float4 sm_o[WPR > 1 ? 8 : 1][V][32];
+    __shared__ float sm_w[8];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int cut = blockIdx.x + 1;
+    Place at;
+    int64_t slot;
+    const int64_t T = locate(
+        p, false, sm_loc, [&](int64_t t) { return cut_at(cut, ctas, t); }, at, slot);
+    if (slot >= T) return;
+    if (T < ctas) ctas = (int)T;
+    const Request r = request_of(p, at.b, false);
+    const int64_t unit = at.off / r.n, into = at.off - unit * r.n;
+    const int64_t first_slot = slot - into;
+    const int64_t prev = cut_at(cut - 1, ctas, T);
+    if (into == 0 || prev > first_slot) return;  // no cut inside a unit, or not its first
+    const int64_t row0 = unit * kM;
+    const int rows = (int)(r.rows - row0 < kM ? r.rows - row0 : kM);
+    const int64_t last = ((first_slot + r.n) * ctas - 1) / T;  // the CTA of the unit's last tile
+    const int n = (int)(last - (cut - 1)) + 1;
+    auto slot_at = [&](int i) { return i == 0 && prev < first_slot ? 2 * (int64_t)(cut - 1) + 1 : 2 * (cut - 1 + (int64_t)i); };
+    const int sub = warp % WPR;
+    const int row = blockIdx.y * RPB + warp / WPR;
+    const bool live = row < rows;
+    float M = -INFINITY, W = 0.f;
+    float4 acc[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v) acc[v] = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (live) {
+        for (int i = lane; i < n; i += 32) M = fmaxf(M, part.lse[slot_at(i) * part.pitch + row]);
+        for (int o = 16; o; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+        if (M != -INFINITY) {
+#pragma unroll 4
+            for (int i = sub; i < n; i += WPR) {
+                const int64_t at_row = slot_at(i) * part.pitch + row;
+                const float w = exp2f((part.lse[at_row] - M) * 1.4426950408889634f);
+                W += w;
+                const float4 *o = reinterpret_cast<const float4 *>(part.o + at_row * R);
+#pragma unroll
+                for (int v = 0; v < V; ++v) {
+                    const float4 x = o[32 * v + lane];
+                    // an empty part (w = 0) holds zeros
+                    acc[v].x = fmaf(w, x.x, acc[v].x);
+                    acc[v].y = fmaf(w, x.y, acc[v].y);
+                    acc[v].z = fmaf(w, x.z, acc[v].z);
+                    acc[v].w = fmaf(w, x.w, acc[v].w);
+                }
+            }
+        }
+    }
+    if (WPR > 1) {
+#pragma unroll
+        for (int v = 0; v < V; ++v) sm_o[warp][v][lane] = acc[v];
+        if (lane == 0) sm_w[warp] = W;
+        __syncthreads();
+        if (sub != 0 || !live) return;
+        for (int k = 1; k < WPR; ++k) {
+            W += sm_w[warp + k];
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                const float4 x = sm_o[warp + k][v][lane];
+                acc[v].x += x.x;
+                acc[v].y += x.y;
+                acc[v].z += x.z;
+                acc[v].w += x.w;
+            }
+        }
+    }
+    if (!live) return;
+    const int64_t out_row = r.q0 * p.num_heads + row0 + row;
+    const float inv = W > 0.f ? 1.f / W : 0.f;
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+        const float4 x = make_float4(acc[v].x * inv, acc[v].y * inv, acc[v].z * inv, acc[v].w * inv);
+        const int64_t e = out_row * R + 128 * v + 4 * lane;
+        if (p.out_dtype == KF_F32) *reinterpret_cast<float4 *>(static_cast<float *>(p.out) + e) = x;
+        else
+            *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(p.out) + e) =
+                make_uint2(pack_bf16(x.x, x.y), pack_bf16(x.z, x.w));
+    }
+    if (lane == 0 && p.lse_out) p.lse_out[out_row] = W > 0.f ? M + logf(W) : -INFINITY;
+}
+
+int64_t row_pitch(int max_query_len, int num_heads) {
+    const int64_t rows = (int64_t)max_query_len * num_heads;
+    return rows < kM ? rows : kM;
+}
+
+// (64 columns, rows, column atoms): a box of 64 rows x all columns lands as atoms of
+// 64 rows x 128 swizzled bytes.
+bool encode_q(tc::EncodeFn fn, CUtensorMap *map, const LatentParams &p) {
+    const int width = p.latent_dim + kRopeDim;
+    const cuuint64_t dims[3] = {64, (cuuint64_t)p.num_q_tokens * p.num_heads, (cuuint64_t)width / 64};
+    const cuuint64_t strides[2] = {(cuuint64_t)width * 2, 128};
+    const cuuint32_t box[3] = {64, (cuuint32_t)kM, (cuuint32_t)width / 64};
+    const cuuint32_t estr[3] = {1, 1, 1};
+    return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<uint16_t *>(p.q), dims, strides, box, estr,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// (64 columns, 8 tokens, column atoms, 8-token groups of all blocks): a box of one
+// block lands group by group, each group atom by atom.
+bool encode_cache(tc::EncodeFn fn, CUtensorMap *map, const LatentParams &p) {
+    const cuuint64_t row = (cuuint64_t)(p.latent_dim + kRopeDim) * 2;
+    const cuuint64_t dims[4] = {64, 8, row / 128, (cuuint64_t)p.num_blocks * (p.block_size / 8)};
+    const cuuint64_t strides[3] = {row, 128, 8 * row};
+    const cuuint32_t box[4] = {64, 8, (cuuint32_t)(row / 128), (cuuint32_t)p.block_size / 8};
+    const cuuint32_t estr[4] = {1, 1, 1, 1};
+    return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<uint16_t *>(p.cache), dims, strides, box, estr,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int R>
+cudaError_t launch(const LatentParams &p, const Partials &part, int ctas, bool long_units, cudaStream_t stream,
+                   const CUtensorMap &mx, const CUtensorMap &mq) {
+    using Sh = LShape<R>;
+    static std::atomic<uint64_t> done{0};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const uint64_t bit = 1ull << (dev & 63);
+    if (!(done.load() & bit)) {
+        e = cudaFuncSetAttribute(latent_kernel<R>, cudaFuncAttributeMaxDynamicSharedMemorySize, Sh::kSmemBytes);
+        if (e != cudaSuccess) return e;
+        done.fetch_or(bit);
+    }
+    latent_kernel<R><<<ctas, kThreads, Sh::kSmemBytes, stream>>>(p, part, mx, mq);
+    e = cudaGetLastError();
+    if (e != cudaSuccess || ctas == 1) return e;
+    if (long_units)
+        latent_merge_kernel<R, 1><<<dim3(ctas - 1, part.pitch), 256, 0, stream>>>(p, part, ctas);
+    else
+        latent_merge_kernel<R, 8><<<dim3(ctas - 1, (part.pitch + 7) / 8), 256, 0, stream>>>(p, part, ctas);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+size_t latent_workspace_bytes(int batch, int max_query_len, int num_heads, int latent_dim, int sm_count) {
+    const size_t rows = 2 * (size_t)sm_count * row_pitch(max_query_len, num_heads);
+    return (rows * latent_dim * 4 + 255) / 256 * 256 + rows * 4;
+}
+
+cudaError_t launch_latent(const LatentParams &p, void *workspace, int sm_count, cudaStream_t stream, void *encode_fn) {
+    tc::EncodeFn fn = reinterpret_cast<tc::EncodeFn>(encode_fn);
+    CUtensorMap mx, mq;
+    if (!encode_cache(fn, &mx, p) || !encode_q(fn, &mq, p)) return cudaErrorInvalidValue;
+    // no more CTAs than the batch can have tiles
+    const int64_t units = (int64_t)p.batch * (((int64_t)p.max_query_len * p.num_heads + kM - 1) / kM);
+    const int64_t tiles = units * std::max<int64_t>(1, ((int64_t)p.max_context_len + kN - 1) / kN);
+    const int ctas = (int)std::min<int64_t>(sm_count, tiles);
+    Partials part;
+    part.pitch = (int)row_pitch(p.max_query_len, p.num_heads);
+    part.o = static_cast<float *>(workspace);
+    const size_t rows = 2 * (size_t)sm_count * part.pitch;
+    part.lse = reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + (rows * p.latent_dim * 4 + 255) / 256 * 256);
+    // few units are cut over many CTAs each: one row a merge block, its warps share
+    // the partials; many units have two or three partials: one warp a row
+    const bool long_units = units * 8 < ctas;
+    return p.latent_dim == 512 ? launch<512>(p, part, ctas, long_units, stream, mx, mq)
+                               : launch<256>(p, part, ctas, long_units, stream, mx, mq);
+}
+
+}  // namespace kf
