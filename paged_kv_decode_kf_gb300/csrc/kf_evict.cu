@@ -9,9 +9,23 @@
 //
 // Selection: the rank order as an unsigned 32-bit key (protected = all ones; a
 // float's bits with the sign folded; NaN = 0, below -inf; -0 = +0). The keep-th
-// largest key comes from a radix search, 8 bits a pass, over a histogram in
-// shared memory; keys equal to it stay in index order until `keep` are found.
-// Then one pass in index order lists holes and movers with block-wide scans.
+// largest key comes from a radix search, 8 bits a pass, over histograms in shared
+// memory (eight copies a bin, by lane: scores share their exponents, and one
+// copy would serialise the atomics); keys equal to it stay in index order until
+// `keep` are found. Two scans then place holes and movers in their lists.
+//
+// One cluster of CL CTAs a request, each with a contiguous part of its tokens,
+// whose keys stay in shared memory from one global read on (up to 49152 a CTA;
+// beyond, every pass computes them again). Histograms and counts meet through
+// distributed shared memory, one cluster barrier a pass. CL = 1 up to 8192
+// tokens, where barriers across CTAs would cost more than they save; 8 above.
+//
+// What bounds it: 4 bytes a token to select (8 with positions), 2 row_bytes a moved
+// row and cache. The selection of a short request is latency: a chain of four
+// passes and two scans.
+#include <algorithm>
+#include <atomic>
+
 #include "kf_evict.cuh"
 
 namespace kf {
@@ -34,7 +48,30 @@ struct Keys {
     }
 };
 
-// Exclusive prefix sum of `x` over the block, and the block's total.
+__device__ __forceinline__ uint32_t cluster_rank() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+
+template <int CL>
+__device__ __forceinline__ void cluster_sync() {
+    if (CL == 1) __syncthreads();
+    else asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+// The int at `p` (shared memory) in CTA `rank` of the cluster.
+template <int CL>
+__device__ __forceinline__ int remote(const int *p, int rank) {
+    if (CL == 1) return *p;
+    uint32_t a = static_cast<uint32_t>(__cvta_generic_to_shared(p)), r;
+    int v;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(rank));
+    asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(r) : "memory");
+    return v;
+}
+
+// Exclusive prefix sum of `x` over the block.
 __device__ __forceinline__ int block_scan(int x, int *warp_sums, int &total) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     int v = x;
@@ -45,142 +82,268 @@ __device__ __forceinline__ int block_scan(int x, int *warp_sums, int &total) {
     __syncthreads();  // warp_sums is free again
     if (lane == 31) warp_sums[warp] = v;
     __syncthreads();
-    if (warp == 0) {
+    int before = 0, all = 0;
+    {
         int w = warp_sums[lane];
-        for (int o = 1; o < 32; o <<= 1) {
-            const int y = __shfl_up_sync(0xffffffffu, w, o);
-            if (lane >= o) w += y;
-        }
-        warp_sums[lane] = w;
+        all = w;
+        for (int o = 16; o; o >>= 1) all += __shfl_xor_sync(0xffffffffu, all, o);
+        w = lane < warp ? w : 0;
+        for (int o = 16; o; o >>= 1) w += __shfl_xor_sync(0xffffffffu, w, o);
+        before = w;
     }
-    __syncthreads();
-    total = warp_sums[31];
-    return v - x + (warp ? warp_sums[warp - 1] : 0);
+    total = all;
+    return v - x + before;
 }
 
+__device__ __forceinline__ void move_row(const EvictParams &p, int b, int src, int dst, int lane) {
+    const int32_t *table = p.block_tables + (int64_t)b * p.bt_stride;
+    const int64_t ps = table[src / p.block_size], pd = table[dst / p.block_size];
+    if (ps < 0 || ps >= p.num_blocks || pd < 0 || pd >= p.num_blocks) {
+        if (lane == 0) raise_error(p.err, KF_DEVERR_BLOCK_ID);
+        return;
+    }
+    const int64_t from = (ps * p.block_size + src % p.block_size) * p.row_vecs;
+    const int64_t to = (pd * p.block_size + dst % p.block_size) * p.row_vecs;
+    // both caches' vectors in flight before the first store: 4 KB a warp
+    for (int v0 = 0; v0 < p.row_vecs; v0 += 128) {
+        uint4 x[2][4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int v = v0 + 32 * i + lane;
+            if (v < p.row_vecs) {
+                x[0][i] = p.cache_a[from + v];
+                if (p.cache_b) x[1][i] = p.cache_b[from + v];
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int v = v0 + 32 * i + lane;
+            if (v < p.row_vecs) {
+                p.cache_a[to + v] = x[0][i];
+                if (p.cache_b) p.cache_b[to + v] = x[1][i];
+            }
+        }
+    }
+}
+
+constexpr int kKeyCap = 49152;  // keys a CTA keeps in shared memory
+constexpr int kCopies = 8;
+
+// MOVE: the kernel moves the rows too (few of them; no second launch).
+template <int CL, bool MOVE>
 __global__ void __launch_bounds__(kSelThreads)
-evict_select_kernel(const EvictParams p) {
-    __shared__ int hist[256];
+evict_select_kernel(const EvictParams p, int key_slots) {
+    __shared__ int hist[256 * kCopies];
+    __shared__ int sums[2][256];  // this CTA's histogram, double-buffered over passes
     __shared__ int warp_sums[32];
-    __shared__ uint32_t s_key;
-    __shared__ int s_left;
-    const int b = blockIdx.x, tid = threadIdx.x;
-    int64_t L = p.ctx_lens[b];
-    __syncthreads();  // every thread has read the length: ctx_out may be the same array
+    __shared__ int s_digit, s_left;
+    __shared__ int s_counts[2];   // this CTA's holes and movers
+    extern __shared__ uint32_t keys[];
+    const int b = blockIdx.x / CL, tid = threadIdx.x;
+    const int rank = CL == 1 ? 0 : (int)cluster_rank();
+    int64_t L64 = p.ctx_lens[b];
+    cluster_sync<CL>();  // every thread has read the length: ctx_out may be the same array
     const int64_t cap = (int64_t)p.bt_stride * p.block_size;
-    if (L < 0 || L > cap) {
-        if (tid == 0) raise_error(p.err, KF_DEVERR_CONTEXT_LEN);
-        L = L < 0 ? 0 : cap;
+    const bool report = rank == 0 && tid == 0;
+    if (L64 < 0 || L64 > cap) {
+        if (report) raise_error(p.err, KF_DEVERR_CONTEXT_LEN);
+        L64 = L64 < 0 ? 0 : cap;
     }
-    if (L > p.max_context_len) {
-        if (tid == 0) raise_error(p.err, KF_DEVERR_MAX_CONTEXT);
-        L = p.max_context_len;
+    if (L64 > p.max_context_len) {
+        if (report) raise_error(p.err, KF_DEVERR_MAX_CONTEXT);
+        L64 = p.max_context_len;
     }
+    const int L = (int)L64;
     const float *scores = p.scores + b * p.score_stride;
     float *scores_out = p.scores_out + b * p.score_stride;
     const int32_t *positions = p.positions ? p.positions + b * p.score_stride : nullptr;
     int32_t *positions_out = p.positions_out ? p.positions_out + b * p.score_stride : nullptr;
     const int keep = p.keep;
+    const int per = (L + CL - 1) / CL;                 // this CTA's tokens: [lo, hi)
+    const int lo = min(rank * per, L), hi = min(lo + per, L);
+    // what stays below `keep` keeps its score and position (movers come after)
+    for (int t = lo + tid; t < min(hi, keep); t += kSelThreads) {
+        scores_out[t] = scores[t];
+        if (positions) positions_out[t] = positions[t];
+    }
     if (L <= keep) {
-        for (int64_t t = tid; t < L; t += kSelThreads) {
-            scores_out[t] = scores[t];
-            if (positions) positions_out[t] = positions[t];
-        }
-        if (tid == 0) {
+        if (report) {
             p.counts[b] = 0;
-            p.ctx_out[b] = (int32_t)L;
+            p.ctx_out[b] = L;
         }
         return;
     }
-    Keys key{scores, positions, p.sink, (positions ? (int64_t)p.seq_lens[b] : L) - p.recent};
+    const Keys key{scores, positions, p.sink, (positions ? (int64_t)p.seq_lens[b] : (int64_t)L) - p.recent};
+    const bool cached = per <= key_slots;
+    if (cached)
+        for (int t = lo + tid; t < hi; t += kSelThreads) keys[t - lo] = key(t);
+    auto key_at = [&](int t) { return cached ? keys[t - lo] : key(t); };
 
     // the keep-th largest key, from its highest byte down
     uint32_t prefix = 0;
     int left = keep;  // how many of the keys that share the prefix stay
-    for (int shift = 24; shift >= 0; shift -= 8) {
-        if (tid < 256) hist[tid] = 0;
+    int eq_before = 0;
+    for (int pass = 0; pass < 4; ++pass) {
+        const int shift = 24 - 8 * pass;
+        for (int i = tid; i < 256 * kCopies; i += kSelThreads) hist[i] = 0;
         __syncthreads();
-        for (int64_t t = tid; t < L; t += kSelThreads) {
-            const uint32_t k = key(t);
-            if (shift == 24 || (k >> (shift + 8)) == (prefix >> (shift + 8)))
-                atomicAdd(&hist[(k >> shift) & 255], 1);
+        for (int t = lo + tid; t < hi; t += kSelThreads) {
+            const uint32_t k = key_at(t);
+            if (pass == 0 || (k >> (shift + 8)) == (prefix >> (shift + 8)))
+                atomicAdd(&hist[((k >> shift) & 255) * kCopies + (tid & (kCopies - 1))], 1);
         }
         __syncthreads();
-        if (tid == 0) {
-            int n = left, d = 255;
-            while (d > 0 && hist[d] < n) n -= hist[d--];
-            s_key = prefix | ((uint32_t)d << shift);
-            s_left = n;
+        int *mine = sums[pass & 1];
+        if (tid < 256) {
+            int n = 0;
+#pragma unroll
+            for (int i = 0; i < kCopies; ++i) n += hist[tid * kCopies + i];
+            mine[tid] = n;
+        }
+        cluster_sync<CL>();
+        // warp 0 finds the digit: lane l holds bins 255 - 8 l down to 248 - 8 l
+        if (tid < 32) {
+            int bin[8], n = 0;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                bin[i] = 0;
+#pragma unroll
+                for (int r = 0; r < CL; ++r) bin[i] += remote<CL>(&mine[255 - 8 * tid - i], r);
+                n += bin[i];
+            }
+            int above = n;  // inclusive sum from the largest digit down
+            for (int o = 1; o < 32; o <<= 1) {
+                const int y = __shfl_up_sync(0xffffffffu, above, o);
+                if (tid >= o) above += y;
+            }
+            int at = above - n;
+            if (at < left && left <= above) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    if (at < left && left <= at + bin[i]) {
+                        s_digit = 255 - 8 * tid - i;
+                        s_left = left - at;
+                    }
+                    at += bin[i];
+                }
+            }
         }
         __syncthreads();
-        prefix = s_key;
+        prefix |= (uint32_t)s_digit << shift;
         left = s_left;
-        __syncthreads();
+        if (pass == 3)
+            for (int r = 0; r < rank; ++r) eq_before += remote<CL>(&mine[prefix & 255], r);
     }
 
-    // in index order: which tokens stay, the holes below `keep` and the movers above it
-    int *dst = p.dst + (int64_t)b * p.max_moves, *src = p.src + (int64_t)b * p.max_moves;
-    int seen_eq = 0, holes = 0, movers = 0;
-    for (int64_t t0 = 0; t0 < L; t0 += kSelThreads) {
-        const int64_t t = t0 + tid;
-        const uint32_t k = t < L ? key(t) : 0u;
-        const bool eq = t < L && k == prefix;
-        int total;
-        const int rank = seen_eq + block_scan(eq, warp_sums, total);
-        seen_eq += total;
-        const bool kept = t < L && (k > prefix || (eq && rank < left));
-        const bool hole = t < keep && !kept, mover = t >= keep && kept;
-        // t < keep and t >= keep never mix in one thread: one scan of both counts, 16 bits each
-        int both;
-        const int at = block_scan((hole ? 1 : 0) + (mover ? 1 << 16 : 0), warp_sums, both);
-        if (hole) dst[holes + (at & 0xffff)] = (int)t;
-        if (mover) src[movers + (at >> 16)] = (int)t;
-        holes += both & 0xffff;
-        movers += both >> 16;
-        if (t < keep && kept) {
-            scores_out[t] = scores[t];
-            if (positions) positions_out[t] = positions[t];
+    // which tokens stay: each thread takes a run of this CTA's tokens, in order
+    // (an odd length: neighbours' reads fall into different banks)
+    const int len = ((per + kSelThreads - 1) / kSelThreads) | 1;
+    const int t0 = min(lo + tid * len, hi), t1 = min(t0 + len, hi);
+    int eq = 0;
+    for (int t = t0; t < t1; ++t) eq += key_at(t) == prefix;
+    int total;
+    const int eq_rank = eq_before + block_scan(eq, warp_sums, total);
+    int holes = 0, movers = 0;
+    {
+        int e = eq_rank;
+        for (int t = t0; t < t1; ++t) {
+            const uint32_t k = key_at(t);
+            const bool kept = k > prefix || (k == prefix && e++ < left);
+            holes += t < keep && !kept;
+            movers += t >= keep && kept;
         }
     }
-    __syncthreads();
-    for (int i = tid; i < movers; i += kSelThreads) {
+    int all_holes, all_movers;
+    int hole_at = block_scan(holes, warp_sums, all_holes), mover_at = block_scan(movers, warp_sums, all_movers);
+    if (CL > 1) {
+        if (tid == 0) {
+            s_counts[0] = all_holes;
+            s_counts[1] = all_movers;
+        }
+        cluster_sync<CL>();
+        all_movers = 0;
+        for (int r = 0; r < CL; ++r) {
+            const int m = remote<CL>(&s_counts[1], r);
+            if (r < rank) {
+                hole_at += remote<CL>(&s_counts[0], r);
+                mover_at += m;
+            }
+            all_movers += m;
+        }
+    }
+    int *dst = p.dst + (int64_t)b * p.max_moves, *src = p.src + (int64_t)b * p.max_moves;
+    {
+        int e = eq_rank;
+        for (int t = t0; t < t1; ++t) {
+            const uint32_t k = key_at(t);
+            const bool kept = k > prefix || (k == prefix && e++ < left);
+            if (t < keep && !kept) dst[hole_at++] = t;
+            if (t >= keep && kept) src[mover_at++] = t;
+        }
+    }
+    if (report) {
+        p.counts[b] = all_movers;
+        p.ctx_out[b] = keep;
+    }
+    cluster_sync<CL>();  // lists complete; no CTA leaves while another reads its shared memory
+    for (int i = rank * kSelThreads + tid; i < all_movers; i += CL * kSelThreads) {
         scores_out[dst[i]] = scores[src[i]];
         if (positions) positions_out[dst[i]] = positions[src[i]];
     }
-    if (tid == 0) {
-        p.counts[b] = movers;
-        p.ctx_out[b] = keep;
-    }
+    if (MOVE)
+        for (int i = rank * (kSelThreads / 32) + (tid >> 5); i < all_movers; i += CL * (kSelThreads / 32))
+            move_row(p, b, src[i], dst[i], tid & 31);
 }
 
 // One warp a moved row.
 __global__ void __launch_bounds__(256)
 evict_move_kernel(const EvictParams p) {
-    const int b = blockIdx.y, lane = threadIdx.x & 31;
+    const int b = blockIdx.y;
     const int i = blockIdx.x * 8 + (threadIdx.x >> 5);
     if (i >= p.counts[b]) return;
-    int64_t row[2];
-    const int tok[2] = {p.src[(int64_t)b * p.max_moves + i], p.dst[(int64_t)b * p.max_moves + i]};
-    for (int k = 0; k < 2; ++k) {
-        const int64_t phys = p.block_tables[(int64_t)b * p.bt_stride + tok[k] / p.block_size];
-        if (phys < 0 || phys >= p.num_blocks) {
-            if (lane == 0) raise_error(p.err, KF_DEVERR_BLOCK_ID);
-            return;
-        }
-        row[k] = (phys * p.block_size + tok[k] % p.block_size) * p.row_vecs;
+    move_row(p, b, p.src[(int64_t)b * p.max_moves + i], p.dst[(int64_t)b * p.max_moves + i], threadIdx.x & 31);
+}
+
+template <int CL, bool MOVE>
+cudaError_t launch_select(const EvictParams &p, cudaStream_t stream) {
+    const int per = (p.max_context_len + CL - 1) / CL;
+    const int slots = std::min(per, kKeyCap);
+    const size_t smem = (size_t)slots * 4;
+    static std::atomic<uint64_t> done{0};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const uint64_t bit = 1ull << (dev & 63);
+    if (!(done.load() & bit)) {
+        e = cudaFuncSetAttribute(evict_select_kernel<CL, MOVE>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 kKeyCap * 4);
+        if (e != cudaSuccess) return e;
+        done.fetch_or(bit);
     }
-    for (int v = lane; v < p.row_vecs; v += 32) {
-        p.cache_a[row[1] + v] = p.cache_a[row[0] + v];
-        if (p.cache_b) p.cache_b[row[1] + v] = p.cache_b[row[0] + v];
-    }
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(p.batch * CL);
+    cfg.blockDim = dim3(kSelThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim = {CL, 1, 1};
+    cfg.attrs = attr;
+    cfg.numAttrs = CL > 1 ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, evict_select_kernel<CL, MOVE>, p, slots);
 }
 
 }  // namespace
 
 cudaError_t launch_evict(const EvictParams &p, int sm_count, cudaStream_t stream) {
-    evict_select_kernel<<<p.batch, kSelThreads, 0, stream>>>(p);
-    cudaError_t e = cudaGetLastError();
-    if (e != cudaSuccess || p.max_moves == 0) return e;
+    // a few moved rows a request are cheaper in the selecting CTA than in a launch of
+    // their own
+    const bool in_place = p.max_moves <= 64;
+    const bool wide = p.max_context_len > 8192;
+    cudaError_t e;
+    if (in_place) e = wide ? launch_select<8, true>(p, stream) : launch_select<1, true>(p, stream);
+    else e = wide ? launch_select<8, false>(p, stream) : launch_select<1, false>(p, stream);
+    if (e != cudaSuccess || in_place) return e;
     evict_move_kernel<<<dim3((p.max_moves + 7) / 8, p.batch), 256, 0, stream>>>(p);
     return cudaGetLastError();
 }

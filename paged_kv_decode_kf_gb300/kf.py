@@ -454,18 +454,29 @@ def _latent_dims(latent_cache: torch.Tensor) -> Tuple[int, int, int, int]:
 
 
 def _shape(t: torch.Tensor, shape, name: str) -> None:
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError("%s must be %s, got %s" % (name, list(shape), list(t.shape)))
 
 
-def _same_device(first: torch.Tensor, *rest) -> torch.cuda.device:
-    """Guard that makes the tensors' device current; they must share one."""
-    for t in rest:
-        if t is not None and t.device != first.device:
-            raise ValueError("all tensors must be on %s, got one on %s" % (first.device, t.device))
-    if not first.is_cuda:
+# The current stream's handle of a device; the public call builds a Stream object
+# first, several microseconds on a slow host core.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _call(name: str, tensors, stream, *args) -> None:
+    """Call the library's `name` with the tensors' device current (they must share
+    one) and the stream appended to the arguments."""
+    index = tensors[0].get_device()
+    if index < 0:
         raise ValueError("all tensors must be CUDA tensors")
-    return torch.cuda.device(first.device)
+    for t in tensors:
+        if t is not None and t.get_device() != index:
+            raise ValueError("all tensors must be on cuda:%d, got one on %s" % (index, t.device))
+    if index != torch.cuda.current_device():
+        with torch.cuda.device(index):
+            return _call(name, tensors, stream, *args)
+    handle = _raw_stream(index) if stream is None and _raw_stream is not None else _stream(stream)
+    _check(getattr(_lib, name)(*args, handle), name)
 
 
 def _opt(t: Optional[torch.Tensor], dtype, name: str) -> Optional[int]:
@@ -488,12 +499,10 @@ def kf_append_latent(latent_new: torch.Tensor, latent_cache: torch.Tensor, block
         _shape(row_start, (B + 1,), "row_start")
     elif n != B:
         raise ValueError("latent_new must hold one row a request without row_start")
-    with _same_device(latent_cache, latent_new, block_tables, context_lens_before, row_start):
-        _check(_lib.kf_append_latent(
-            _dev(latent_new, torch.bfloat16, "latent_new"), _opt(row_start, torch.int32, "row_start"),
-            _dev(latent_cache, torch.bfloat16, "latent_cache"), _dev(block_tables, torch.int32, "block_tables"),
-            block_tables.shape[1], _dev(context_lens_before, torch.int32, "context_lens_before"), B, n, r, rope, bs,
-            nb, _stream(stream)), "kf_append_latent")
+    _call("kf_append_latent", (latent_cache, latent_new, block_tables, context_lens_before, row_start), stream,
+          _dev(latent_new, torch.bfloat16, "latent_new"), _opt(row_start, torch.int32, "row_start"),
+          _dev(latent_cache, torch.bfloat16, "latent_cache"), _dev(block_tables, torch.int32, "block_tables"),
+          block_tables.shape[1], _dev(context_lens_before, torch.int32, "context_lens_before"), B, n, r, rope, bs, nb)
 
 
 def kf_latent_workspace_size(batch: int, max_query_len: int, num_heads: int, latent_dim: int) -> int:
@@ -545,14 +554,13 @@ def kf_latent_attention(q: torch.Tensor, latent_cache: torch.Tensor, block_table
     nb, bs, r, rope = _latent_dims(latent_cache)
     out, code, lse_out = _latent_call(q, r + rope, r, block_tables, context_lens, q_start, out, out_dtype, lse_out,
                                       want_lse)
-    with _same_device(q, latent_cache, block_tables, context_lens, workspace, q_start, out, lse_out):
-        _check(_lib.kf_latent_attention(
-            _dev(q, torch.bfloat16, "q"), _opt(q_start, torch.int32, "q_start"),
-            _dev(latent_cache, torch.bfloat16, "latent_cache"), _dev(block_tables, torch.int32, "block_tables"),
-            block_tables.shape[1], _dev(context_lens, torch.int32, "context_lens"), int(bool(causal)),
-            int(max_context_len), int(max_query_len), block_tables.shape[0], q.shape[0], q.shape[1], r, rope, bs, nb,
-            float(scale), _dev(workspace, torch.uint8, "workspace"), workspace.numel(), _dev(out, out.dtype, "out"),
-            code, _opt(lse_out, torch.float32, "lse_out"), _stream(stream)), "kf_latent_attention")
+    _call("kf_latent_attention", (q, latent_cache, block_tables, context_lens, workspace, q_start, out, lse_out), stream,
+          _dev(q, torch.bfloat16, "q"), _opt(q_start, torch.int32, "q_start"),
+          _dev(latent_cache, torch.bfloat16, "latent_cache"), _dev(block_tables, torch.int32, "block_tables"),
+          block_tables.shape[1], _dev(context_lens, torch.int32, "context_lens"), int(bool(causal)),
+          int(max_context_len), int(max_query_len), block_tables.shape[0], q.shape[0], q.shape[1], r, rope, bs, nb,
+          float(scale), _dev(workspace, torch.uint8, "workspace"), workspace.numel(), _dev(out, out.dtype, "out"),
+          code, _opt(lse_out, torch.float32, "lse_out"))
     return out, lse_out
 
 
@@ -586,16 +594,15 @@ def kf_latent_attention_expanded(q: torch.Tensor, latent_cache: torch.Tensor, w_
                                       want_lse)
     _shape(w_uk, (q.shape[1], dn, r), "w_uk")
     _shape(w_uv, (q.shape[1], dv, r), "w_uv")
-    with _same_device(q, latent_cache, w_uk, w_uv, block_tables, context_lens, workspace, q_start, out, lse_out):
-        _check(_lib.kf_latent_attention_expanded(
-            _dev(q, torch.bfloat16, "q"), _opt(q_start, torch.int32, "q_start"),
-            _dev(latent_cache, torch.bfloat16, "latent_cache"), _dev(w_uk, torch.bfloat16, "w_uk"),
-            _dev(w_uv, torch.bfloat16, "w_uv"), _dev(block_tables, torch.int32, "block_tables"),
-            block_tables.shape[1], _dev(context_lens, torch.int32, "context_lens"), int(bool(causal)),
-            int(max_context_len), int(max_query_len), block_tables.shape[0], q.shape[0], q.shape[1], r, rope, dn, dv,
-            bs, nb, float(scale), _dev(workspace, torch.uint8, "workspace"), workspace.numel(),
-            _dev(out, out.dtype, "out"), code, _opt(lse_out, torch.float32, "lse_out"), _stream(stream)),
-            "kf_latent_attention_expanded")
+    _call("kf_latent_attention_expanded",
+          (q, latent_cache, w_uk, w_uv, block_tables, context_lens, workspace, q_start, out, lse_out), stream,
+          _dev(q, torch.bfloat16, "q"), _opt(q_start, torch.int32, "q_start"),
+          _dev(latent_cache, torch.bfloat16, "latent_cache"), _dev(w_uk, torch.bfloat16, "w_uk"),
+          _dev(w_uv, torch.bfloat16, "w_uv"), _dev(block_tables, torch.int32, "block_tables"),
+          block_tables.shape[1], _dev(context_lens, torch.int32, "context_lens"), int(bool(causal)),
+          int(max_context_len), int(max_query_len), block_tables.shape[0], q.shape[0], q.shape[1], r, rope, dn, dv,
+          bs, nb, float(scale), _dev(workspace, torch.uint8, "workspace"), workspace.numel(),
+          _dev(out, out.dtype, "out"), code, _opt(lse_out, torch.float32, "lse_out"))
     return out, lse_out
 
 
@@ -618,15 +625,14 @@ def _accumulate(name, q, k_cache, k_scale, block_tables, context_lens, max_conte
     if k_scale is not None:
         _shape(k_scale, (hkv,), "k_scale")
     cache = _dev(k_cache, torch.bfloat16, "k_cache") if k_scale is None else _dev8(k_cache, "k_cache")
-    with _same_device(q, k_cache, k_scale, block_tables, context_lens, lse, scores_out, scores_in, q_start):
-        scales = () if k_scale is None else (_dev(k_scale, torch.float32, "k_scale"),)
-        _check(getattr(_lib, name)(
-            _dev(q, torch.bfloat16, "q"), _opt(q_start, torch.int32, "q_start"), cache, *scales,
-            _dev(block_tables, torch.int32, "block_tables"), block_tables.shape[1],
-            _dev(context_lens, torch.int32, "context_lens"), int(bool(causal)), int(max_context_len),
-            int(max_query_len), B, nq, hq, hkv, d, bs, nb, float(scale), _dev(lse, torch.float32, "lse"),
-            _opt(scores_in, torch.float32, "scores_in"), _dev(scores_out, torch.float32, "scores_out"),
-            scores_out.shape[1], _stream(stream)), name)
+    scales = () if k_scale is None else (_dev(k_scale, torch.float32, "k_scale"),)
+    _call(name, (q, k_cache, k_scale, block_tables, context_lens, lse, scores_out, scores_in, q_start), stream,
+          _dev(q, torch.bfloat16, "q"), _opt(q_start, torch.int32, "q_start"), cache, *scales,
+          _dev(block_tables, torch.int32, "block_tables"), block_tables.shape[1],
+          _dev(context_lens, torch.int32, "context_lens"), int(bool(causal)), int(max_context_len),
+          int(max_query_len), B, nq, hq, hkv, d, bs, nb, float(scale), _dev(lse, torch.float32, "lse"),
+          _opt(scores_in, torch.float32, "scores_in"), _dev(scores_out, torch.float32, "scores_out"),
+          scores_out.shape[1])
     return scores_out
 
 
@@ -676,7 +682,7 @@ def kf_evict_tokens(caches, block_tables: torch.Tensor, context_lens: torch.Tens
         if c.dim() < 3 or c.shape != first.shape or c.dtype != first.dtype:
             raise ValueError("caches must share one [num_blocks, block_size, ...] shape and type")
     nb, bs = first.shape[:2]
-    row_bytes = first[0, 0].numel() * first.element_size() if nb and bs else 0
+    row_bytes = first.stride(1) * first.element_size()
     B = block_tables.shape[0]
     for t, n in ((context_lens, "context_lens"), (context_lens_out, "context_lens_out"), (seq_lens, "seq_lens")):
         if t is not None:
@@ -686,17 +692,16 @@ def kf_evict_tokens(caches, block_tables: torch.Tensor, context_lens: torch.Tens
     for t, n in ((scores_out, "scores_out"), (positions, "positions"), (positions_out, "positions_out")):
         if t is not None:
             _shape(t, scores.shape, n)
-    with _same_device(*caches, block_tables, context_lens, scores, context_lens_out, scores_out, workspace, positions,
-                      seq_lens, positions_out):
-        ptr = [_dev(c, c.dtype, "caches") for c in caches] + [None]
-        _check(_lib.kf_evict_tokens(
-            ptr[0], ptr[1], row_bytes, _dev(block_tables, torch.int32, "block_tables"), block_tables.shape[1],
-            _dev(context_lens, torch.int32, "context_lens"), int(max_context_len), B, bs, nb,
-            _dev(scores, torch.float32, "scores"), _dev(scores_out, torch.float32, "scores_out"), scores.shape[1],
-            _opt(positions, torch.int32, "positions"), _opt(positions_out, torch.int32, "positions_out"),
-            _opt(seq_lens, torch.int32, "seq_lens"), int(keep), int(sink), int(recent),
-            _dev(context_lens_out, torch.int32, "context_lens_out"), _dev(workspace, torch.uint8, "workspace"),
-            workspace.numel(), _stream(stream)), "kf_evict_tokens")
+    ptr = [_dev(c, c.dtype, "caches") for c in caches] + [None]
+    _call("kf_evict_tokens", (*caches, block_tables, context_lens, scores, context_lens_out, scores_out, workspace,
+                              positions, seq_lens, positions_out), stream,
+          ptr[0], ptr[1], row_bytes, _dev(block_tables, torch.int32, "block_tables"), block_tables.shape[1],
+          _dev(context_lens, torch.int32, "context_lens"), int(max_context_len), B, bs, nb,
+          _dev(scores, torch.float32, "scores"), _dev(scores_out, torch.float32, "scores_out"), scores.shape[1],
+          _opt(positions, torch.int32, "positions"), _opt(positions_out, torch.int32, "positions_out"),
+          _opt(seq_lens, torch.int32, "seq_lens"), int(keep), int(sink), int(recent),
+          _dev(context_lens_out, torch.int32, "context_lens_out"), _dev(workspace, torch.uint8, "workspace"),
+          workspace.numel())
 
 
 def kf_check_bounded_wait(stream=None) -> None:
