@@ -21,11 +21,13 @@ LIB = os.path.join(LIBDIR, "libkf.so")
 SOURCES = ["kf_api.cu", "kf_append.cu", "kf_merge.cu", "kf_decode_simt.cu", "kf_decode_tc.cu",
            "kf_decode_tc_fp8.cu", "kf_decode_bal.cu", "kf_decode_bal_fp8.cu", "kf_multiquery.cu",
            "kf_multiquery_tc05.cu", "kf_multiquery_tc05w.cu", "kf_multiquery_tc05p.cu", "kf_static.cu",
-           "kf_latent_api.cu", "kf_latent_append.cu", "kf_latent.cu", "kf_latent_tc05.cu", "kf_accumulate.cu", "kf_evict.cu"]
+           "kf_latent_api.cu", "kf_latent_append.cu", "kf_latent_tc05.cu",
+           "kf_latent_expand.cu", "kf_latent_expanded.cu", "kf_accumulate.cu", "kf_evict.cu"]
 HEADERS = [os.path.join(CSRC, "kf_internal.cuh"), os.path.join(CSRC, "kf_decode_tc.cuh"),
            os.path.join(CSRC, "kf_decode_bal.cuh"),
            os.path.join(CSRC, "kf_tc05.cuh"), os.path.join(CSRC, "kf_mq_tc05.cuh"),
-           os.path.join(CSRC, "kf_latent.cuh"), os.path.join(CSRC, "kf_evict.cuh"),
+           os.path.join(CSRC, "kf_latent.cuh"), os.path.join(CSRC, "kf_latent_expanded.cuh"),
+           os.path.join(CSRC, "kf_runs.cuh"), os.path.join(CSRC, "kf_evict.cuh"),
            os.path.join(ROOT, "include", "kf.h")]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ARCH + ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-I" + os.path.join(ROOT, "include")]

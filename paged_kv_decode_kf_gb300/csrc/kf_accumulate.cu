@@ -28,6 +28,7 @@
 // warp; a tile never crosses a cache block (16 or 32 tokens).
 #include "kf_decode_tc.cuh"
 #include "kf_evict.cuh"
+#include "kf_runs.cuh"
 
 namespace kf {
 namespace {
@@ -86,48 +87,23 @@ accumulate_kernel(const AccumulateParams p) {
     constexpr int NL = KV8 ? D / 64 : D / 32;   // 16-byte loads a lane and K row
     constexpr int NQ = D / 32;                  // 16-byte loads a lane and q row
     constexpr int EB = KV8 ? 1 : 2;
-    __shared__ int64_t sm_sum[kWarps], sm_at[2];
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    __shared__ int64_t sm_loc[36];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int g = lane >> 2, t4 = lane & 3;
 
-    // this CTA's first tile: prefix sums of the requests' tile counts over the block
-    const int per = (p.batch + 32 * kWarps - 1) / (32 * kWarps);
-    const int b0 = min(tid * per, p.batch), b1 = min(b0 + per, p.batch);
-    int64_t mine = 0;
-    for (int b = b0; b < b1; ++b) mine += (acc_request(p, b, blockIdx.x == 0).L + 15) / 16;
-    int64_t v = mine;
-    for (int o = 1; o < 32; o <<= 1) {
-        const int64_t y = __shfl_up_sync(0xffffffffu, v, o);
-        if (lane >= o) v += y;
-    }
-    if (lane == 31) sm_sum[warp] = v;
-    __syncthreads();
-    int64_t before = v - mine, total = 0;
-    for (int w = 0; w < kWarps; ++w) {
-        if (w < warp) before += sm_sum[w];
-        total += sm_sum[w];
-    }
+    // runs are cut for warps; this CTA's first one starts at `at`
     const int64_t runs = (int64_t)gridDim.x * kWarps;
-    const int64_t cta_first = (int64_t)blockIdx.x * kWarps * total / runs;
-    if (cta_first >= before && cta_first < before + mine) {
-        int64_t at = before;
-        for (int b = b0; b < b1; ++b) {
-            const int64_t n = (acc_request(p, b, false).L + 15) / 16;
-            if (cta_first < at + n) {
-                sm_at[0] = b;
-                sm_at[1] = at;
-                break;
-            }
-            at += n;
-        }
-    }
-    __syncthreads();
+    Place at;
+    int64_t cta_first;
+    const int64_t total = locate(
+        p.batch, [&](int b) { return (acc_request(p, b, blockIdx.x == 0).L + 15) / 16; }, sm_loc,
+        [&](int64_t T) { return (int64_t)blockIdx.x * kWarps * T / runs; }, at, cta_first);
     const int64_t run = (int64_t)blockIdx.x * kWarps + warp;
     int64_t idx = run * total / runs;
     const int64_t end = (run + 1) * total / runs;
     if (idx >= end) return;
-    int b = (int)sm_at[0];
-    int64_t req_first = sm_at[1];  // the request's first tile in the batch's list
+    int b = at.b;
+    int64_t req_first = cta_first - at.off;  // the request's first tile in the batch's list
     AccRequest r = acc_request(p, b, false);
     const int G = p.num_q_heads / p.num_kv_heads;
     const int log_g = 31 - __clz(G);

@@ -44,6 +44,7 @@
 // drains its copies and MMAs, frees its TMEM and returns.
 #include "kf_latent.cuh"
 #include "kf_mq_tc05.cuh"
+#include "kf_runs.cuh"
 
 #include <algorithm>
 
@@ -96,60 +97,9 @@ __device__ __forceinline__ Request request_of(const LatentParams &p, int b, bool
     return q;
 }
 
-// The first tile of CTA i's run when T tiles are cut into min(ctas, T) equal runs
-// (CTAs past the last run have none).
-__device__ __forceinline__ int64_t cut_at(int i, int ctas, int64_t T) {
-    const int64_t P = ctas < T ? ctas : T;
-    return i < P ? i * T / P : T;
-}
-
-struct Place {
-    int b;
-    int64_t off;  // tiles into the request
-};
-
-// Where the batch's tile `slot_of(T)` lies, and T. All threads of the block (whole
-// warps, at most 1024) call it; `sm` holds 36 int64.
-template <typename F>
-__device__ __forceinline__ int64_t locate(const LatentParams &p, bool report, int64_t *sm, F slot_of, Place &place,
-                                          int64_t &slot) {
-    const int tid = threadIdx.x, nt = blockDim.x, lane = tid & 31, warp = tid >> 5;
-    const int per = (p.batch + nt - 1) / nt;
-    const int b0 = min(tid * per, p.batch), b1 = min(b0 + per, p.batch);
-    int64_t mine = 0;
-    for (int b = b0; b < b1; ++b) {
-        const Request r = request_of(p, b, report);
-        mine += r.n * r.units;
-    }
-    int64_t v = mine;
-    for (int o = 1; o < 32; o <<= 1) {
-        const int64_t y = __shfl_up_sync(0xffffffffu, v, o);
-        if (lane >= o) v += y;
-    }
-    if (lane == 31) sm[warp] = v;
-    __syncthreads();
-    int64_t before = v - mine, total = 0;
-    for (int w = 0; w < nt / 32; ++w) {
-        if (w < warp) before += sm[w];
-        total += sm[w];
-    }
-    slot = slot_of(total);
-    if (slot >= before && slot < before + mine) {
-        int64_t at = before;
-        for (int b = b0; b < b1; ++b) {
-            const Request r = request_of(p, b, false);
-            if (slot < at + r.n * r.units) {
-                sm[34] = b;
-                sm[35] = slot - at;
-                break;
-            }
-            at += r.n * r.units;
-        }
-    }
-    __syncthreads();
-    place.b = (int)sm[34];
-    place.off = sm[35];
-    return total;
+__device__ __forceinline__ int64_t cost_of(const LatentParams &p, int b, bool report) {
+    const Request r = request_of(p, b, report);
+    return r.n * r.units;
 }
 
 // One unit's part in a CTA's run: token tiles [tile0, tile0 + tiles).
@@ -249,21 +199,6 @@ __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
         : "memory");
 }
 
-__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap *map, int x, int y, int z, uint32_t bar) {
-    asm volatile(
-        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-        " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(bar)
-        : "memory");
-}
-
-// One lane of a converged warp (the same one every time).
-__device__ __forceinline__ bool elect_one() {
-    uint32_t r;
-    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
-    return r != 0;
-}
-
 // The softmax warps' barrier, and the same with an OR of one predicate.
 __device__ __forceinline__ void soft_sync() { asm volatile("barrier.cta.sync 1, 128;" ::: "memory"); }
 
@@ -332,7 +267,8 @@ latent_kernel(const LatentParams p, const Partials part, const __grid_constant__
     Walker walk;
     int64_t slot0;
     const int64_t total = locate(
-        p, blockIdx.x == 0, sm_loc, [&](int64_t T) { return cut_at(blockIdx.x, gridDim.x, T); }, walk.at, slot0);
+        p.batch, [&](int b) { return cost_of(p, b, blockIdx.x == 0); }, sm_loc,
+        [&](int64_t T) { return cut_at(blockIdx.x, gridDim.x, T); }, walk.at, slot0);
     walk.left = cut_at(blockIdx.x + 1, gridDim.x, total) - slot0;
     if (abort_flag) walk.left = 0;  // an earlier kernel's wait gave up (no role has started yet)
     tc05::fence_before_sync();
@@ -659,7 +595,7 @@ latent_merge_kernel(const LatentParams p, const Partials part, int ctas) {
     Place at;
     int64_t slot;
     const int64_t T = locate(
-        p, false, sm_loc, [&](int64_t t) { return cut_at(cut, ctas, t); }, at, slot);
+        p.batch, [&](int b) { return cost_of(p, b, false); }, sm_loc, [&](int64_t t) { return cut_at(cut, ctas, t); }, at, slot);
     if (slot >= T) return;
     if (T < ctas) ctas = (int)T;
     const Request r = request_of(p, at.b, false);
