@@ -191,27 +191,32 @@ expanded_kernel(const LatentParams p, const ExpandedKV kv, int q_tiles, const __
         for (int j = 0; ok && j <= ntiles; ++j) {
             const bool has_s = j < ntiles, has_pv = j > 0;
             const uint32_t st = j % NS, pst = (j + NS - 1) % NS;
-            ok = !__any_sync(0xffffffffu, abort_flag) && (!has_s || warp_wait(full(st), (j / NS) & 1));
-            if (!ok) break;
             const uint64_t kd = tc05::sdesc_sw128(sKV + st * Sh::kStageBytes, 16, 1024);
             const uint64_t vd = tc05::sdesc_sw128(sKV + pst * Sh::kStageBytes + Sh::kVAt, Sh::kAtomBytes, 1024);
             for (int t = 0; t < nqt; ++t) {
-                if (has_pv && !warp_wait(p_full(t), (j - 1) & 1)) {
-                    ok = false;
-                    break;
-                }
-                tc05::fence_after_sync();
                 const uint32_t s = tm + Sh::col_s(t), q = tm + Sh::col_q(t);
-                const uint64_t qd = tc05::sdesc_sw128(sQ + t * kRows * 128, 16, 1024);
-                if (elect_one()) {
-                    if (has_pv) {
+                if (has_pv) {
+                    ok = warp_wait(p_full(t), (j - 1) & 1);
+                    if (!ok) break;
+                    tc05::fence_after_sync();
+                    if (elect_one()) {
 #pragma unroll
                         for (int kk = 0; kk < kTok / 16; ++kk)
                             tc05::mma_ts(tm + Sh::col_o(t), s + 8 * kk, vd + (uint64_t)(kk * 2048 / 16), id_o,
                                          (j > 1 || kk > 0) ? 1u : 0u);
                         if (t == nqt - 1) tc05::commit(empty(pst));
                     }
-                    if (has_s) {
+                    __syncwarp();
+                }
+                // (the stage has nearly always landed: its wait runs under the value product)
+                if (t == 0 && has_s) {
+                    ok = !__any_sync(0xffffffffu, abort_flag) && warp_wait(full(st), (j / NS) & 1);
+                    if (!ok) break;
+                    tc05::fence_after_sync();
+                }
+                if (has_s) {
+                    const uint64_t qd = tc05::sdesc_sw128(sQ + t * kRows * 128, 16, 1024);
+                    if (elect_one()) {
 #pragma unroll
                         for (int kk = 0; kk < 2 * DN / 16; ++kk)  // q_n against hi, then against lo
                             tc05::mma_ts(s, q + 8 * (kk % (DN / 16)),
@@ -223,8 +228,8 @@ expanded_kernel(const LatentParams p, const ExpandedKV kv, int q_tiles, const __
                                          kd + (uint64_t)((Sh::kRopeAt + 32 * kk) / 16), id_s, 1u);
                         tc05::commit(s_full(t));
                     }
+                    __syncwarp();
                 }
-                __syncwarp();
             }
         }
         if (elect_one()) {

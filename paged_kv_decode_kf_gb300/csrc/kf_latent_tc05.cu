@@ -15,7 +15,7 @@
 // them. So a batch of any length mix keeps every SM busy to the end, at the
 // price of at most two partials a CTA.
 //
-// One tile: 64 x (R + 64) bf16 arrive as one TMA box a cache block, landing as
+// One tile: 64 x (R + 64) bf16 arrive as four TMA boxes of 16 tokens, landing as
 // 8-token groups of 128-byte-swizzled atoms (group, 64-column atom, token, column).
 //   S[64 rows x 64 tokens]     = Q X^T          A = Q, B = X, both K-major, M = 64
 //   O^T[128 columns x rows]   += C^T P^T        A = C^T (M-major: the same tile), B = P
@@ -56,6 +56,7 @@ using namespace mq5;
 
 constexpr int kM = 64;   // rows a unit
 constexpr int kN = 64;   // tokens a tile
+constexpr int kAhead = 2;  // tiles fetched into L2 ahead of the ring's loads
 constexpr int kSoftThreads = 128, kProducerWarp = 4, kScoreWarp = 5, kValueWarp = 6, kThreads = 224;
 
 template <int R>
@@ -109,11 +110,13 @@ struct Segment {
     int t_end;          // the last token any row of the unit sees, plus one
     int b;
     bool whole, first;  // the unit lies in this run alone; it is the run's first segment
+    bool cut;           // the unit starts here and goes on in the next run
+    int64_t unit_end;   // the tile after the unit's last, in the batch's list
 };
 
 struct Walker {
     Place at;
-    int64_t left;
+    int64_t pos, left;  // the next tile in the batch's list; tiles left of the run
     bool first = true;
     Request r;
     bool loaded = false;
@@ -141,6 +144,8 @@ struct Walker {
             s.b = at.b;
             s.whole = len == r.n;
             s.first = first;
+            s.cut = tile == 0 && !s.whole;
+            s.unit_end = pos - tile + r.n;
             int64_t end = r.L;
             if (p.causal) {
                 const int64_t lim = r.shift + (s.row0 + s.rows - 1) / p.num_heads + 1;
@@ -152,6 +157,7 @@ struct Walker {
             s.tile0 = (int)tile;
             s.tiles = hi > tile ? (int)(hi - tile) : 0;
             at.off += len;
+            pos += len;
             left -= len;
             first = false;
             return true;
@@ -160,9 +166,17 @@ struct Walker {
     }
 };
 
+// A unit cut over CTAs first .. first + parts - 1: where its partials lie. The first
+// CTA's slot is `slot0`; the others' is the first of their two (2 i).
+struct Cut {
+    int64_t row_out;  // its first row in out and lse_out
+    int rows, parts, slot0, pad;
+};
+
 struct Partials {
     float *o;    // [2 * CTAs][row pitch][R]
     float *lse;  // [2 * CTAs][row pitch]
+    Cut *cuts;   // [CTAs]: the unit that starts in CTA i's run and goes on (parts = 0: none)
     int pitch;   // rows a slot holds
 };
 
@@ -199,6 +213,14 @@ __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
         : "memory");
 }
 
+// A 4-D box into L2.
+__device__ __forceinline__ void prefetch_4d(const CUtensorMap *map, int x, int y, int z, int w) {
+    asm volatile("cp.async.bulk.prefetch.tensor.4d.L2.global.tile [%0, {%1, %2, %3, %4}];" ::"l"(
+                     reinterpret_cast<uint64_t>(map)),
+                 "r"(x), "r"(y), "r"(z), "r"(w)
+                 : "memory");
+}
+
 // The softmax warps' barrier, and the same with an OR of one predicate.
 __device__ __forceinline__ void soft_sync() { asm volatile("barrier.cta.sync 1, 128;" ::: "memory"); }
 
@@ -211,6 +233,32 @@ __device__ __forceinline__ bool soft_any(bool x) {
         : "r"((uint32_t)x)
         : "memory");
     return r != 0;
+}
+
+// put(row, column offset, value) for this thread's column of every 128-column tile
+// and the first `rows` rows: O^T times the row's 1 / sum (in `inv`), or zeros.
+template <int R, typename F>
+__device__ __forceinline__ void store_rows(uint32_t tm, bool any, int rows, const float *inv, F put) {
+    for (int d = 0; d < R / 128; ++d) {
+        for (int r0 = 0; r0 < rows; r0 += 32) {
+            uint32_t o[32];
+            if (any) tc05::tmem_ld32(tm + 64 * d + r0, o);
+            if (any && r0 + 32 <= rows) {
+#pragma unroll
+                for (int e = 0; e < 32; ++e) {
+                    const float w = inv[r0 + e];
+                    put(r0 + e, 128 * d, w > 0.f ? __uint_as_float(o[e]) * w : 0.f);
+                }
+            } else {
+#pragma unroll
+                for (int e = 0; e < 32; ++e)
+                    if (r0 + e < rows) {
+                        const float w = inv[r0 + e];
+                        put(r0 + e, 128 * d, any && w > 0.f ? __uint_as_float(o[e]) * w : 0.f);
+                    }
+            }
+        }
+    }
 }
 
 // ---------------------------------------------------------------------------
@@ -269,6 +317,7 @@ latent_kernel(const LatentParams p, const Partials part, const __grid_constant__
     const int64_t total = locate(
         p.batch, [&](int b) { return cost_of(p, b, blockIdx.x == 0); }, sm_loc,
         [&](int64_t T) { return cut_at(blockIdx.x, gridDim.x, T); }, walk.at, slot0);
+    walk.pos = slot0;
     walk.left = cut_at(blockIdx.x + 1, gridDim.x, total) - slot0;
     if (abort_flag) walk.left = 0;  // an earlier kernel's wait gave up (no role has started yet)
     tc05::fence_before_sync();
@@ -292,27 +341,35 @@ latent_kernel(const LatentParams p, const Partials part, const __grid_constant__
 
     if (warp == kProducerWarp) {
         // ------------------------------ producer ------------------------------
-        const uint32_t box_bytes = (uint32_t)p.block_size * (R + kRopeDim) * 2;
-        const int max_blk = kN >> bs_shift;
         uint32_t g = 0, nseg = 0, q_loads = 0;
         bool ok = true;
-        Segment s;
+        Segment s{};
+        // lane e < 4: the cache row group of the tile's e-th 16 tokens, asked for long
+        // before the tile's turn; past the last token any valid one
+        auto group_of = [&](int tile) -> int {
+            const int t = tile * kN + 16 * lane;
+            if (lane >= kN / 16 || t >= s.t_end) return -1;
+            const int64_t e = t >> bs_shift;
+            int64_t phys = e < p.bt_stride ? p.block_tables[(int64_t)s.b * p.bt_stride + e] : -1;
+            if (phys < 0 || phys >= p.num_blocks) {
+                raise_error(p.err, KF_DEVERR_BLOCK_ID);
+                phys = 0;
+            }
+            return (int)(phys * (p.block_size / 8)) + ((t & (p.block_size - 1)) >> 3);
+        };
         while (ok && walk.next(p, s)) {
             if (s.tiles == 0) continue;
+            // kAhead tiles beyond the ring are fetched into L2: HBM's latency then passes
+            // under their predecessors' turns, and the ring's own loads come from L2
+            int grp[kAhead + 1];
+#pragma unroll
+            for (int k = 0; k < kAhead; ++k) grp[k] = k < s.tiles ? group_of(s.tile0 + k) : -1;
             for (int i = 0; i < s.tiles; ++i, ++g) {
+                grp[kAhead] = i + kAhead < s.tiles ? group_of(s.tile0 + i + kAhead) : -1;
+                if (grp[kAhead] >= 0) prefetch_4d(&tmap_x, 0, 0, 0, grp[kAhead]);
                 const int t0 = (s.tile0 + i) * kN;
                 const int ntok = s.t_end - t0 < kN ? s.t_end - t0 : kN;
-                const int nblk = (ntok + p.block_size - 1) >> bs_shift;
-                // this tile's table entries, asked for before the wait for its slot
-                int64_t phys = 0;
-                if (lane < max_blk && lane < nblk) {
-                    const int64_t e = (t0 >> bs_shift) + lane;
-                    phys = e < p.bt_stride ? p.block_tables[(int64_t)s.b * p.bt_stride + e] : -1;
-                    if (phys < 0 || phys >= p.num_blocks) {
-                        raise_error(p.err, KF_DEVERR_BLOCK_ID);
-                        phys = 0;
-                    }
-                }
+                const int nbox = (ntok + 15) / 16;
                 const uint32_t st = g % NS;
                 int go = 1;
                 if (lane == 0) {
@@ -325,7 +382,7 @@ latent_kernel(const LatentParams p, const Partials part, const __grid_constant__
                             tma_load_3d(sQ, &tmap_q, 0, (int)(s.q0 * p.num_heads + s.row0), 0, q_full);
                         }
                     }
-                    if (go) mbar_arrive_expect_tx(full(st), nblk * box_bytes);
+                    if (go) mbar_arrive_expect_tx(full(st), nbox * 2 * Sh::kGroupBytes);
                     else {
                         raise_error(p.err, KF_DEVERR_TIMEOUT);
                         abort_flag = 1;
@@ -333,10 +390,12 @@ latent_kernel(const LatentParams p, const Partials part, const __grid_constant__
                 }
                 ok = __shfl_sync(0xffffffffu, go, 0);
                 if (!ok) break;
-                if (lane < nblk)
-                    tma_load_4d(sX + st * Sh::kTileBytes + lane * box_bytes, &tmap_x, 0, 0, 0,
-                                (int)(phys * (p.block_size / 8)), full(st));
+                if (lane < nbox)
+                    tma_load_4d(sX + st * Sh::kTileBytes + lane * 2 * Sh::kGroupBytes, &tmap_x, 0, 0, 0, grp[0],
+                                full(st));
                 __syncwarp();
+#pragma unroll
+                for (int k = 0; k < kAhead; ++k) grp[k] = grp[k + 1];
             }
             ++nseg;
         }
@@ -354,7 +413,7 @@ latent_kernel(const LatentParams p, const Partials part, const __grid_constant__
         const uint64_t qd = tc05::sdesc_sw128(sQ, 16, 1024);
         uint32_t g = 0, nseg = 0;
         bool ok = true;
-        Segment s;
+        Segment s{};
         while (ok && walk.next(p, s)) {
             const int tiles = __shfl_sync(0xffffffffu, s.tiles, 0);
             if (tiles == 0) continue;
@@ -385,7 +444,7 @@ latent_kernel(const LatentParams p, const Partials part, const __grid_constant__
         const uint64_t pd = tc05::sdesc_sw128(sP, 16, 1024);
         uint32_t g = 0, nseg = 0;
         bool ok = true;
-        Segment s;
+        Segment s{};
         while (ok && walk.next(p, s)) {
             const int tiles = __shfl_sync(0xffffffffu, s.tiles, 0);
             if (tiles == 0) continue;
@@ -421,7 +480,8 @@ latent_kernel(const LatentParams p, const Partials part, const __grid_constant__
         const int rr[2] = {16 * warp + (lane >> 2), 16 * warp + (lane >> 2) + 8};  // this lane's rows
         uint32_t g = 0;
         bool fail = false, stop = false;  // fail: this warp's wait gave up; stop: all four warps leave
-        Segment s;
+        Cut cut{};
+        Segment s{};
         while (!stop && walk.next(p, s)) {
             float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
             int lim[2];  // tokens these rows see (none: rows past the unit's last)
@@ -455,17 +515,30 @@ latent_kernel(const LatentParams p, const Partials part, const __grid_constant__
                     }
                 }
                 float mx[2] = {-INFINITY, -INFINITY};
+                // fast path: both rows see the whole tile (so does the quad: lim goes by row)
+                // and the scale is positive; otherwise scores are scaled and masked first
+                const bool fast = c > 0.f && __all_sync(0xffffffffu, t0 + kN <= lim[0] && t0 + kN <= lim[1]);
+                if (fast) {
 #pragma unroll
-                for (int e = 0; e < 8; ++e)
+                    for (int e = 0; e < 8; ++e)
 #pragma unroll
-                    for (int k = 0; k < 2; ++k)
+                        for (int k = 0; k < 2; ++k)
+                            mx[k] = max3f(mx[k], __uint_as_float(x[4 * e + 2 * k]), __uint_as_float(x[4 * e + 2 * k + 1]));
+                    mx[0] *= c;
+                    mx[1] *= c;
+                } else {
 #pragma unroll
-                        for (int u = 0; u < 2; ++u) {
-                            const int t = t0 + 8 * e + 2 * (lane & 3) + u;
-                            const float v = t < lim[k] ? __uint_as_float(x[4 * e + 2 * k + u]) * c : -INFINITY;
-                            x[4 * e + 2 * k + u] = __float_as_uint(v);
-                            mx[k] = fmaxf(mx[k], v);
-                        }
+                    for (int e = 0; e < 8; ++e)
+#pragma unroll
+                        for (int k = 0; k < 2; ++k)
+#pragma unroll
+                            for (int u = 0; u < 2; ++u) {
+                                const int t = t0 + 8 * e + 2 * (lane & 3) + u;
+                                const float v = t < lim[k] ? __uint_as_float(x[4 * e + 2 * k + u]) * c : -INFINITY;
+                                x[4 * e + 2 * k + u] = __float_as_uint(v);
+                                mx[k] = fmaxf(mx[k], v);
+                            }
+                }
                 bool need = false;
                 float alpha[2];
 #pragma unroll
@@ -507,16 +580,22 @@ latent_kernel(const LatentParams p, const Partials part, const __grid_constant__
 #pragma unroll
                 for (int k = 0; k < 2; ++k) {
                     const float mu = m[k] == -INFINITY ? 0.f : m[k];
+                    const float cc = fast ? c : 1.f;  // (scores are scaled already on the slow path)
                     const uint32_t row = sP + rr[k] * 128;
+                    float2 ls = make_float2(0.f, 0.f);
 #pragma unroll
                     for (int e = 0; e < 8; ++e) {
-                        const float a = ex2f(__uint_as_float(x[4 * e + 2 * k]) - mu);
-                        const float b = ex2f(__uint_as_float(x[4 * e + 2 * k + 1]) - mu);
-                        l[k] += a + b;
+                        float2 a = fma_f32x2(
+                            make_float2(__uint_as_float(x[4 * e + 2 * k]), __uint_as_float(x[4 * e + 2 * k + 1])),
+                            make_float2(cc, cc), make_float2(-mu, -mu));
+                        a.x = ex2f(a.x);
+                        a.y = ex2f(a.y);
+                        ls = add_f32x2(ls, a);
                         asm volatile("st.shared.u32 [%0], %1;" ::"r"(row + ((e ^ (rr[k] & 7)) << 4) + (lane & 3) * 4),
-                                     "r"(pack_bf16(a, b))
+                                     "r"(pack_bf16(a.x, a.y))
                                      : "memory");
                     }
+                    l[k] += ls.x + ls.y;
                 }
                 fence_proxy_async_smem();
                 tc05::fence_before_sync();
@@ -538,23 +617,23 @@ latent_kernel(const LatentParams p, const Partials part, const __grid_constant__
             if (stop) break;
             const int64_t slot = 2 * (int64_t)blockIdx.x + (s.first ? 0 : 1);
             const int64_t row_out = s.q0 * p.num_heads + s.row0;
+            if (s.cut) {
+                const int64_t P = (int64_t)gridDim.x < total ? gridDim.x : total;
+                const int64_t last = (s.unit_end * P - 1) / total;  // the CTA of the unit's last tile
+                cut = Cut{row_out, s.rows, (int)(last - blockIdx.x) + 1, (int)slot, 0};
+            }
             if (s.tiles > 0) tc05::fence_after_sync();
-            for (int d = 0; d < Sh::kDimTiles; ++d) {
-                const int dim = 128 * d + threadIdx.x;
-                for (int q = 0; q < (s.rows + 15) / 16; ++q) {
-                    uint32_t o[16];
-                    if (s.tiles > 0) tmem_ld16(tm + lane_base + 64 * d + 16 * q, o);
-#pragma unroll
-                    for (int e = 0; e < 16; ++e) {
-                        const int r = 16 * q + e;
-                        const float inv = sm_alpha[r];
-                        const float v = s.tiles > 0 && inv > 0.f ? __uint_as_float(o[e]) * inv : 0.f;
-                        if (r >= s.rows) continue;
-                        if (!s.whole) part.o[(slot * part.pitch + r) * R + dim] = v;
-                        else if (p.out_dtype == KF_F32) static_cast<float *>(p.out)[(row_out + r) * R + dim] = v;
-                        else static_cast<__nv_bfloat16 *>(p.out)[(row_out + r) * R + dim] = __float2bfloat16(v);
-                    }
-                }
+            // O^T: thread = column, one row a TMEM column; 32 consecutive numbers a warp and store
+            if (!s.whole) {
+                float *dst = part.o + slot * part.pitch * R + threadIdx.x;
+                store_rows<R>(tm + lane_base, s.tiles > 0, s.rows, sm_alpha, [=](int r, int d, float v) { dst[r * R + d] = v; });
+            } else if (p.out_dtype == KF_F32) {
+                float *dst = static_cast<float *>(p.out) + row_out * R + threadIdx.x;
+                store_rows<R>(tm + lane_base, s.tiles > 0, s.rows, sm_alpha, [=](int r, int d, float v) { dst[r * R + d] = v; });
+            } else {
+                __nv_bfloat16 *dst = static_cast<__nv_bfloat16 *>(p.out) + row_out * R + threadIdx.x;
+                store_rows<R>(tm + lane_base, s.tiles > 0, s.rows, sm_alpha,
+                              [=](int r, int d, float v) { dst[r * R + d] = __float2bfloat16(v); });
             }
             if (threadIdx.x < s.rows) {
                 if (!s.whole) part.lse[slot * part.pitch + threadIdx.x] = sm_lse[threadIdx.x];
@@ -564,11 +643,16 @@ latent_kernel(const LatentParams p, const Partials part, const __grid_constant__
             if (s.tiles > 0) mbar_arrive(o_empty);
             soft_sync();  // sm_alpha and sm_lse are free again
         }
+        if (threadIdx.x == 0) {
+            if (stop) cut.parts = 0;
+            part.cuts[blockIdx.x] = cut;
+        }
         if (stop) {
             if (threadIdx.x == 0) raise_error(p.err, KF_DEVERR_TIMEOUT);
             abort_flag = 1;
         }
     }
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the merge may be set up
     tc05::fence_before_sync();
     __syncthreads();
     if (warp == kScoreWarp) {
@@ -578,36 +662,23 @@ latent_kernel(const LatentParams p, const Partials part, const __grid_constant__
 }
 
 // ---------------------------------------------------------------------------
-// Merge of the units that more than one CTA worked on. Block x handles the unit
-// cut at the start of CTA x + 1's run, if that is the unit's first cut; RPB rows
-// a block, 8 / RPB warps a row, each over every (8 / RPB)-th partial:
+// Merge of the units that more than one CTA worked on: block x takes the one that
+// CTA x began, RPB rows a block, 8 / RPB warps a row, each over every (8 / RPB)-th
+// partial:
 //   M = max lse_i, w_i = e^{lse_i - M}, out = sum w_i o_i / sum w_i.
 // ---------------------------------------------------------------------------
 template <int R, int RPB>
 __global__ void __launch_bounds__(256)
-latent_merge_kernel(const LatentParams p, const Partials part, int ctas) {
+latent_merge_kernel(const LatentParams p, const Partials part) {
     constexpr int WPR = 8 / RPB, V = R / 128;  // warps a row; float4 a lane
-    __shared__ int64_t sm_loc[36];
     __shared__ float4 sm_o[WPR > 1 ? 8 : 1][V][32];
     __shared__ float sm_w[8];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int cut = blockIdx.x + 1;
-    Place at;
-    int64_t slot;
-    const int64_t T = locate(
-        p.batch, [&](int b) { return cost_of(p, b, false); }, sm_loc, [&](int64_t t) { return cut_at(cut, ctas, t); }, at, slot);
-    if (slot >= T) return;
-    if (T < ctas) ctas = (int)T;
-    const Request r = request_of(p, at.b, false);
-    const int64_t unit = at.off / r.n, into = at.off - unit * r.n;
-    const int64_t first_slot = slot - into;
-    const int64_t prev = cut_at(cut - 1, ctas, T);
-    if (into == 0 || prev > first_slot) return;  // no cut inside a unit, or not its first
-    const int64_t row0 = unit * kM;
-    const int rows = (int)(r.rows - row0 < kM ? r.rows - row0 : kM);
-    const int64_t last = ((first_slot + r.n) * ctas - 1) / T;  // the CTA of the unit's last tile
-    const int n = (int)(last - (cut - 1)) + 1;
-    auto slot_at = [&](int i) { return i == 0 && prev < first_slot ? 2 * (int64_t)(cut - 1) + 1 : 2 * (cut - 1 + (int64_t)i); };
+    asm volatile("griddepcontrol.wait;" ::: "memory");  // the attention kernel's writes are there
+    const Cut cut = part.cuts[blockIdx.x];
+    const int n = cut.parts, rows = cut.rows;
+    if (n == 0 || blockIdx.y * RPB >= rows) return;
+    auto slot_at = [&](int i) { return i == 0 ? (int64_t)cut.slot0 : 2 * ((int64_t)blockIdx.x + i); };
     const int sub = warp % WPR;
     const int row = blockIdx.y * RPB + warp / WPR;
     const bool live = row < rows;
@@ -656,7 +727,7 @@ latent_merge_kernel(const LatentParams p, const Partials part, int ctas) {
         }
     }
     if (!live) return;
-    const int64_t out_row = r.q0 * p.num_heads + row0 + row;
+    const int64_t out_row = cut.row_out + row;
     const float inv = W > 0.f ? 1.f / W : 0.f;
 #pragma unroll
     for (int v = 0; v < V; ++v) {
@@ -688,13 +759,13 @@ bool encode_q(tc::EncodeFn fn, CUtensorMap *map, const LatentParams &p) {
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// (64 columns, 8 tokens, column atoms, 8-token groups of all blocks): a box of one
-// block lands group by group, each group atom by atom.
+// (64 columns, 8 tokens, column atoms, 8-token groups of all blocks): a box of 16
+// tokens (which no block border cuts) lands group by group, each atom by atom.
 bool encode_cache(tc::EncodeFn fn, CUtensorMap *map, const LatentParams &p) {
     const cuuint64_t row = (cuuint64_t)(p.latent_dim + kRopeDim) * 2;
     const cuuint64_t dims[4] = {64, 8, row / 128, (cuuint64_t)p.num_blocks * (p.block_size / 8)};
     const cuuint64_t strides[3] = {row, 128, 8 * row};
-    const cuuint32_t box[4] = {64, 8, (cuuint32_t)(row / 128), (cuuint32_t)p.block_size / 8};
+    const cuuint32_t box[4] = {64, 8, (cuuint32_t)(row / 128), 2};
     const cuuint32_t estr[4] = {1, 1, 1, 1};
     return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<uint16_t *>(p.cache), dims, strides, box, estr,
               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
@@ -718,18 +789,31 @@ cudaError_t launch(const LatentParams &p, const Partials &part, int ctas, bool l
     latent_kernel<R><<<ctas, kThreads, Sh::kSmemBytes, stream>>>(p, part, mx, mq);
     e = cudaGetLastError();
     if (e != cudaSuccess || ctas == 1) return e;
-    if (long_units)
-        latent_merge_kernel<R, 1><<<dim3(ctas - 1, part.pitch), 256, 0, stream>>>(p, part, ctas);
-    else
-        latent_merge_kernel<R, 8><<<dim3(ctas - 1, (part.pitch + 7) / 8), 256, 0, stream>>>(p, part, ctas);
-    return cudaGetLastError();
+    cudaLaunchConfig_t cfg = {};
+    cfg.blockDim = dim3(256);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;  // set up while the attention kernel ends
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (long_units) {
+        cfg.gridDim = dim3(ctas - 1, part.pitch);
+        return cudaLaunchKernelEx(&cfg, latent_merge_kernel<R, 1>, p, part);
+    }
+    cfg.gridDim = dim3(ctas - 1, (part.pitch + 7) / 8);
+    return cudaLaunchKernelEx(&cfg, latent_merge_kernel<R, 8>, p, part);
 }
 
 }  // namespace
 
+namespace {
+size_t al256(size_t x) { return (x + 255) & ~(size_t)255; }
+}  // namespace
+
 size_t latent_workspace_bytes(int batch, int max_query_len, int num_heads, int latent_dim, int sm_count) {
     const size_t rows = 2 * (size_t)sm_count * row_pitch(max_query_len, num_heads);
-    return (rows * latent_dim * 4 + 255) / 256 * 256 + rows * 4;
+    return al256(rows * latent_dim * 4) + al256(rows * 4) + sm_count * sizeof(Cut);
 }
 
 cudaError_t launch_latent(const LatentParams &p, void *workspace, int sm_count, cudaStream_t stream, void *encode_fn) {
@@ -744,7 +828,9 @@ cudaError_t launch_latent(const LatentParams &p, void *workspace, int sm_count, 
     part.pitch = (int)row_pitch(p.max_query_len, p.num_heads);
     part.o = static_cast<float *>(workspace);
     const size_t rows = 2 * (size_t)sm_count * part.pitch;
-    part.lse = reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + (rows * p.latent_dim * 4 + 255) / 256 * 256);
+    uint8_t *ws = static_cast<uint8_t *>(workspace) + al256(rows * p.latent_dim * 4);
+    part.lse = reinterpret_cast<float *>(ws);
+    part.cuts = reinterpret_cast<Cut *>(ws + al256(rows * 4));
     // few units are cut over many CTAs each: one row a merge block, its warps share
     // the partials; many units have two or three partials: one warp a row
     const bool long_units = units * 8 < ctas;

@@ -91,6 +91,15 @@ __device__ __forceinline__ void commit(uint32_t bar) {
                  : "memory");
 }
 
+// The same arrival on the barrier at offset `bar` of every CTA in `cta_mask`.
+__device__ __forceinline__ void commit_multicast(uint32_t bar, uint16_t cta_mask) {
+    asm volatile(
+        "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+            bar),
+        "h"(cta_mask)
+        : "memory");
+}
+
 // Columns [col, col + 32) of this thread's TMEM lane, waited for. The warp's
 // 32 lanes are lanes 32 * (warp % 4) .. + 31 of `taddr`'s lane field.
 __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[32]) {
