@@ -81,11 +81,129 @@ __device__ __forceinline__ AccRequest acc_request(const AccumulateParams &p, int
     return r;
 }
 
+// Eight columns (j, g) of one KV head as B fragments: lane (g, t4) holds part t4 of
+// column c0 + g; and of its two result columns 2 t4, 2 t4 + 1 the lse, the scale
+// and the last token they see.
+template <int D>
+struct Columns {
+    static constexpr int NQ = D / 32;  // 16-byte loads a lane and q row
+    uint4 q[NQ];
+    float lse2[2], c[2];
+    int hide[2];
+
+    template <bool KV8>
+    __device__ __forceinline__ void load(const AccumulateParams &p, const AccRequest &r, int h, int64_t c0, int64_t cols,
+                                         int log_g, float kscale) {
+        const int lane = threadIdx.x & 31, g = lane >> 2, t4 = lane & 3;
+        const int G = 1 << log_g;
+        const int64_t col = c0 + g;  // zeros past the last
+        const uint16_t *qrow = p.q + (((r.q0 + (col >> log_g)) * p.num_q_heads) + h * G + (col & (G - 1))) * D;
+#pragma unroll
+        for (int i = 0; i < NQ; ++i) {
+            // bf16 K: chunk t4 + 4 i of 8 numbers; E4M3 K: 16 numbers at 16 (t4 + 4 (i / 2))
+            const int e = KV8 ? 16 * (t4 + 4 * (i >> 1)) + 8 * (i & 1) : 8 * (t4 + 4 * i);
+            q[i] = col < cols ? __ldg(reinterpret_cast<const uint4 *>(qrow + e)) : make_uint4(0, 0, 0, 0);
+        }
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+            const int64_t cc = c0 + 2 * t4 + u;
+            float l = INFINITY;  // weight 0
+            if (cc < cols) l = p.lse[(r.q0 + (cc >> log_g)) * p.num_q_heads + h * G + (cc & (G - 1))];
+            lse2[u] = l == -INFINITY ? INFINITY : l * 1.4426950408889634f;
+            hide[u] = (int)(p.causal ? r.shift + (cc >> log_g) : r.L);  // (lengths are 32-bit)
+            c[u] = p.scale_log2;
+        }
+        if (KV8) {
+            float mx = 0.f;
+#pragma unroll
+            for (int i = 0; i < NQ; ++i) {
+                const uint32_t w[4] = {q[i].x, q[i].y, q[i].z, q[i].w};
+#pragma unroll
+                for (int e = 0; e < 4; ++e) mx = fmaxf(mx, fmaxf(fabsf(bf16_lo(w[e])), fabsf(bf16_hi(w[e]))));
+            }
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+            // times 2^(14 - exponent of mx), where both it and its inverse are normal numbers
+            int ex = (int)((__float_as_uint(mx) >> 23) & 255) - 127;
+            ex = ex < -100 ? -100 : ex;
+            const float up = __uint_as_float((uint32_t)(14 - ex + 127) << 23);
+            const float unscale = kscale * __uint_as_float((uint32_t)(ex - 14 + 127) << 23);
+#pragma unroll
+            for (int i = 0; i < NQ; ++i) {
+                uint32_t w[4] = {q[i].x, q[i].y, q[i].z, q[i].w};
+#pragma unroll
+                for (int e = 0; e < 4; ++e) w[e] = pack_f16(bf16_lo(w[e]) * up, bf16_hi(w[e]) * up);
+                q[i] = make_uint4(w[0], w[1], w[2], w[3]);
+            }
+            // (column n's scale lives in lanes 4 n .. 4 n + 3)
+#pragma unroll
+            for (int u = 0; u < 2; ++u) c[u] *= __shfl_sync(0xffffffffu, unscale, 4 * (2 * t4 + u));
+        }
+    }
+};
+
+// sum[k][w] += the weights the eight columns give the tokens t0 + 16 k + g + 8 w.
+template <int D, bool KV8, int T>
+__device__ __forceinline__ void add_columns(const uint4 (&kr)[T][2][KV8 ? D / 64 : D / 32], const Columns<D> &q,
+                                            int t0, float (&sum)[T][2]) {
+    const int g = (threadIdx.x & 31) >> 2;
+#pragma unroll
+    for (int k = 0; k < T; ++k) {
+        float s[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int i = 0; i < (KV8 ? D / 64 : D / 32); ++i) {
+            const uint4 ka = kr[k][0][i], kb = kr[k][1][i];
+            if (KV8) {
+                const uint32_t wa[4] = {ka.x, ka.y, ka.z, ka.w}, wb[4] = {kb.x, kb.y, kb.z, kb.w};
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const uint32_t a[4] = {e4m3x2_to_f16x2(wa[e]), e4m3x2_to_f16x2(wb[e]),
+                                           e4m3x2_to_f16x2(wa[e] >> 16), e4m3x2_to_f16x2(wb[e] >> 16)};
+                    const uint4 qq = q.q[(2 * i + (e >> 1)) % (D / 32)];
+                    if (e & 1) mma_f16(s, a, qq.z, qq.w);
+                    else mma_f16(s, a, qq.x, qq.y);
+                }
+            } else {
+                const uint32_t a0[4] = {ka.x, kb.x, ka.y, kb.y}, a1[4] = {ka.z, kb.z, ka.w, kb.w};
+                mma_bf16(s, a0, q.q[i].x, q.q[i].y);
+                mma_bf16(s, a1, q.q[i].z, q.q[i].w);
+            }
+        }
+        const int t = t0 + 16 * k + g;
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+#pragma unroll
+            for (int w = 0; w < 2; ++w)
+                if (t + 8 * w <= q.hide[u]) sum[k][w] += exp2_approx(fmaf(s[2 * w + u], q.c[u], -q.lse2[u]));
+    }
+}
+
+// This lane's K rows of T 16-token tiles (rows g and g + 8), from part t4 of KV head 0
+// on; tiles past the last repeat it.
+template <int D, bool KV8, int T>
+__device__ __forceinline__ void key_rows(const AccumulateParams &p, int b, int64_t tile0, int tiles,
+                                         const uint8_t *(&row)[T][2]) {
+    const int lane = threadIdx.x & 31, g = lane >> 2, t4 = lane & 3;
+#pragma unroll
+    for (int k = 0; k < T; ++k) {
+        const int64_t t = (tile0 + (k < tiles ? k : tiles - 1)) * 16;
+        int64_t phys = p.block_tables[(int64_t)b * p.bt_stride + t / p.block_size];
+        if (phys < 0 || phys >= p.num_blocks) {
+            if (lane == 0) raise_error(p.err, KF_DEVERR_BLOCK_ID);
+            phys = 0;
+        }
+        const int64_t first = phys * p.block_size + t % p.block_size;
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+            row[k][u] = static_cast<const uint8_t *>(p.k_cache) +
+                        (first + g + 8 * u) * p.num_kv_heads * (D * (KV8 ? 1 : 2)) + t4 * 16;
+    }
+}
+
 template <int D, bool KV8>
 __global__ void __launch_bounds__(32 * kWarps, 4)
 accumulate_kernel(const AccumulateParams p) {
     constexpr int NL = KV8 ? D / 64 : D / 32;   // 16-byte loads a lane and K row
-    constexpr int NQ = D / 32;                  // 16-byte loads a lane and q row
     constexpr int EB = KV8 ? 1 : 2;
     __shared__ int64_t sm_loc[36];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -119,22 +237,8 @@ accumulate_kernel(const AccumulateParams p) {
         int64_t tiles = n - tile0 < end - idx ? n - tile0 : end - idx;
         if (tiles > kTiles) tiles = kTiles;
 
-        // rows of this lane's tokens (tile k, rows g and g + 8)
         const uint8_t *row[kTiles][2];
-#pragma unroll
-        for (int k = 0; k < kTiles; ++k) {
-            const int64_t t = (tile0 + (k < tiles ? k : 0)) * 16;
-            int64_t phys = p.block_tables[(int64_t)b * p.bt_stride + t / p.block_size];
-            if (phys < 0 || phys >= p.num_blocks) {
-                if (lane == 0) raise_error(p.err, KF_DEVERR_BLOCK_ID);
-                phys = 0;
-            }
-            const int64_t first = phys * p.block_size + t % p.block_size;
-#pragma unroll
-            for (int u = 0; u < 2; ++u)
-                row[k][u] = static_cast<const uint8_t *>(p.k_cache) +
-                            (first + g + 8 * u) * p.num_kv_heads * (D * EB) + t4 * 16;
-        }
+        key_rows<D, KV8, kTiles>(p, b, tile0, (int)tiles, row);
         float sum[kTiles][2] = {};
         const int64_t cols = r.C << log_g;
         // with a causal window, columns of queries before the first that sees this tile add nothing
@@ -151,85 +255,9 @@ accumulate_kernel(const AccumulateParams p) {
                         kr[k][u][i] = load_stream(row[k][u] + (int64_t)h * (D * EB) + i * 64);
             const float kscale = KV8 ? p.k_scale[h] : 1.f;
             for (int64_t c0 = col0; c0 < cols; c0 += 8) {
-                // this lane's q row: column c0 + g (zeros past the last)
-                uint4 q[NQ];
-                const int64_t col = c0 + g;
-                const uint16_t *qrow =
-                    p.q + (((r.q0 + (col >> log_g)) * p.num_q_heads) + h * G + (col & (G - 1))) * D;
-#pragma unroll
-                for (int i = 0; i < NQ; ++i) {
-                    // bf16 K: chunk t4 + 4 i of 8 numbers; E4M3 K: 16 numbers at 16 (t4 + 4 (i / 2))
-                    const int e = KV8 ? 16 * (t4 + 4 * (i >> 1)) + 8 * (i & 1) : 8 * (t4 + 4 * i);
-                    q[i] = col < cols ? __ldg(reinterpret_cast<const uint4 *>(qrow + e)) : make_uint4(0, 0, 0, 0);
-                }
-                float unscale = kscale;  // of column c0 + g
-                if (KV8) {
-                    float mx = 0.f;
-#pragma unroll
-                    for (int i = 0; i < NQ; ++i) {
-                        const uint32_t w[4] = {q[i].x, q[i].y, q[i].z, q[i].w};
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) mx = fmaxf(mx, fmaxf(fabsf(bf16_lo(w[e])), fabsf(bf16_hi(w[e]))));
-                    }
-                    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-                    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-                    // 2^(14 - exponent of mx), its exponent kept where both it and its inverse are normal
-                    int ex = (int)((__float_as_uint(mx) >> 23) & 255) - 127;
-                    ex = ex < -100 ? -100 : ex;
-                    const float up = __uint_as_float((uint32_t)(14 - ex + 127) << 23);
-                    unscale *= __uint_as_float((uint32_t)(ex - 14 + 127) << 23);
-#pragma unroll
-                    for (int i = 0; i < NQ; ++i) {
-                        uint32_t w[4] = {q[i].x, q[i].y, q[i].z, q[i].w};
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) w[e] = pack_f16(bf16_lo(w[e]) * up, bf16_hi(w[e]) * up);
-                        q[i] = make_uint4(w[0], w[1], w[2], w[3]);
-                    }
-                }
-                // the two columns of this lane's results: their lse and scale
-                float lse2[2], c[2];
-                int64_t hide[2];  // tokens above this are not seen
-#pragma unroll
-                for (int u = 0; u < 2; ++u) {
-                    const int64_t cc = c0 + 2 * t4 + u;
-                    float l = INFINITY;  // weight 0
-                    if (cc < cols)
-                        l = p.lse[(r.q0 + (cc >> log_g)) * p.num_q_heads + h * G + (cc & (G - 1))];
-                    lse2[u] = l == -INFINITY ? INFINITY : l * 1.4426950408889634f;
-                    // (column n's row maximum lives in lanes 4 n .. 4 n + 3)
-                    c[u] = p.scale_log2 * (KV8 ? __shfl_sync(0xffffffffu, unscale, 4 * (2 * t4 + u)) : 1.f);
-                    hide[u] = p.causal ? r.shift + (cc >> log_g) : r.L;
-                }
-#pragma unroll
-                for (int k = 0; k < kTiles; ++k) {
-                    float s[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                    for (int i = 0; i < NL; ++i) {
-                        const uint4 ka = kr[k][0][i], kb = kr[k][1][i];
-                        if (KV8) {
-                            const uint32_t wa[4] = {ka.x, ka.y, ka.z, ka.w}, wb[4] = {kb.x, kb.y, kb.z, kb.w};
-#pragma unroll
-                            for (int e = 0; e < 4; ++e) {
-                                const uint32_t a[4] = {e4m3x2_to_f16x2(wa[e]), e4m3x2_to_f16x2(wb[e]),
-                                                       e4m3x2_to_f16x2(wa[e] >> 16), e4m3x2_to_f16x2(wb[e] >> 16)};
-                                const uint4 qq = q[2 * i + (e >> 1)];
-                                if (e & 1) mma_f16(s, a, qq.z, qq.w);
-                                else mma_f16(s, a, qq.x, qq.y);
-                            }
-                        } else {
-                            const uint32_t a0[4] = {ka.x, kb.x, ka.y, kb.y}, a1[4] = {ka.z, kb.z, ka.w, kb.w};
-                            mma_bf16(s, a0, q[i].x, q[i].y);
-                            mma_bf16(s, a1, q[i].z, q[i].w);
-                        }
-                    }
-                    const int64_t t = (tile0 + k) * 16 + g;
-#pragma unroll
-                    for (int u = 0; u < 2; ++u)
-#pragma unroll
-                        for (int w = 0; w < 2; ++w)
-                            if (t + 8 * w <= hide[u])
-                                sum[k][w] += exp2_approx(fmaf(s[2 * w + u], c[u], -lse2[u]));
-                }
+                Columns<D> q;
+                q.template load<KV8>(p, r, h, c0, cols, log_g, kscale);
+                add_columns<D, KV8, kTiles>(kr, q, (int)tile0 * 16, sum);
             }
         }
 #pragma unroll
@@ -250,19 +278,122 @@ accumulate_kernel(const AccumulateParams p) {
     }
 }
 
+// Windows of queries (more than eight columns a KV head): one CTA a run of 64 tokens,
+// its eight warps split the (KV head, column group) pairs, so that the tokens' keys
+// are held while the columns pass (128 registers at D = 128) and q, which every CTA
+// reads whole, is read once per 64 tokens. The next group's q is asked for before this
+// one's products. The warps' sums meet in shared memory, in warp order.
+constexpr int kWinWarps = 8, kWinTiles = 4;
+
+template <int D, bool KV8>
+__global__ void __launch_bounds__(32 * kWinWarps, 1)
+accumulate_window_kernel(const AccumulateParams p) {
+    constexpr int NL = KV8 ? D / 64 : D / 32, EB = KV8 ? 1 : 2;
+    __shared__ int64_t sm_loc[36];
+    __shared__ float part[kWinWarps][kWinTiles * 16];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int g = lane >> 2, t4 = lane & 3;
+    const int log_g = 31 - __clz(p.num_q_heads / p.num_kv_heads);
+    auto runs_of = [&](int b, bool report) {
+        return (acc_request(p, b, report).L + 16 * kWinTiles - 1) / (16 * kWinTiles);
+    };
+    Place at;
+    int64_t idx;
+    const int64_t total = locate(
+        p.batch, [&](int b) { return runs_of(b, blockIdx.x == 0); }, sm_loc,
+        [&](int64_t T) { return cut_at(blockIdx.x, gridDim.x, T); }, at, idx);
+    const int64_t end = cut_at(blockIdx.x + 1, gridDim.x, total);
+    int b = at.b;
+    int64_t run = at.off, n = idx < end ? runs_of(b, false) : 0;
+    // warps of one head share its columns; with more heads than warps, heads take turns
+    const int heads = p.num_kv_heads, share = heads < kWinWarps ? kWinWarps / heads : 1;
+    for (; idx < end; ++idx, ++run) {
+        while (run >= n) {  // on to the next request with tokens (it exists: idx < total)
+            run = 0;
+            n = runs_of(++b, false);
+        }
+        const AccRequest r = acc_request(p, b, false);
+        const int64_t t0 = run * 16 * kWinTiles;
+        const int tiles = (int)(((r.L - t0 < 16 * kWinTiles ? r.L - t0 : 16 * kWinTiles) + 15) / 16);
+        const uint8_t *row[kWinTiles][2];
+        key_rows<D, KV8, kWinTiles>(p, b, run * kWinTiles, tiles, row);
+        float sum[kWinTiles][2] = {};
+        const int64_t cols = r.C << log_g;
+        // with a causal window, columns of queries before the first that sees this run add nothing
+        int64_t col0 = 0;
+        if (p.causal && t0 > r.shift) col0 = ((t0 - r.shift) << log_g) & ~7ll;
+        const int64_t step = 8 * share;
+        for (int h = warp / share; h < heads; h += kWinWarps) {
+            int64_t c0 = col0 + 8 * (warp % share);
+            if (c0 >= cols) continue;
+            const float kscale = KV8 ? p.k_scale[h] : 1.f;
+            Columns<D> q;
+            q.template load<KV8>(p, r, h, c0, cols, log_g, kscale);
+            uint4 kr[kWinTiles][2][NL];
+#pragma unroll
+            for (int k = 0; k < kWinTiles; ++k)
+#pragma unroll
+                for (int u = 0; u < 2; ++u)
+#pragma unroll
+                    for (int i = 0; i < NL; ++i) kr[k][u][i] = load_stream(row[k][u] + (int64_t)h * (D * EB) + i * 64);
+            while (true) {
+                Columns<D> next;
+                const bool more = c0 + step < cols;
+                if (more) next.template load<KV8>(p, r, h, c0 + step, cols, log_g, kscale);
+                add_columns<D, KV8, kWinTiles>(kr, q, (int)t0, sum);
+                if (!more) break;
+                q = next;
+                c0 += step;
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < kWinTiles; ++k)
+#pragma unroll
+            for (int w = 0; w < 2; ++w) {
+                float x = sum[k][w];
+                x += __shfl_xor_sync(0xffffffffu, x, 1);
+                x += __shfl_xor_sync(0xffffffffu, x, 2);
+                if (t4 == w) part[warp][16 * k + g + 8 * w] = x;
+            }
+        __syncthreads();
+        const int64_t t = t0 + threadIdx.x;
+        if (threadIdx.x < 16 * kWinTiles && t < r.L) {
+            float x = 0.f;
+#pragma unroll
+            for (int w = 0; w < kWinWarps; ++w) x += part[w][threadIdx.x];
+            const int64_t where = b * p.score_stride + t;
+            p.scores_out[where] = (p.scores_in ? p.scores_in[where] : 0.f) + x;
+        }
+        __syncthreads();
+    }
+}
+
+template <int D, bool KV8>
+void launch(const AccumulateParams &p, int sm_count, cudaStream_t stream) {
+    // Columns a KV head: up to eight are one pass of the row kernel (96 us on 64
+    // requests of 4K with one query); more keep the keys while the columns pass.
+    const int64_t cols = (int64_t)p.max_query_len * (p.num_q_heads / p.num_kv_heads);
+    const int64_t tiles = (int64_t)p.batch * ((p.max_context_len + 15) / 16);
+    // one wave of resident CTAs, no more warps (CTAs) than the batch can have tiles (runs)
+    if (cols <= 8) {
+        const int64_t ctas = (tiles + kWarps - 1) / kWarps < 4ll * sm_count ? (tiles + kWarps - 1) / kWarps : 4ll * sm_count;
+        accumulate_kernel<D, KV8><<<(unsigned)ctas, 32 * kWarps, 0, stream>>>(p);
+    } else {
+        const int64_t runs = (int64_t)p.batch * ((p.max_context_len + 16 * kWinTiles - 1) / (16 * kWinTiles));
+        accumulate_window_kernel<D, KV8>
+            <<<(unsigned)(runs < sm_count ? runs : sm_count), 32 * kWinWarps, 0, stream>>>(p);
+    }
+}
+
 }  // namespace
 
 cudaError_t launch_accumulate(const AccumulateParams &p, int sm_count, cudaStream_t stream) {
-    // one wave of resident CTAs, no more warps than the batch can have tiles
-    const int64_t tiles = (int64_t)p.batch * ((p.max_context_len + 15) / 16);
-    const int64_t ctas = (tiles + kWarps - 1) / kWarps < 4ll * sm_count ? (tiles + kWarps - 1) / kWarps : 4ll * sm_count;
-    const dim3 grid((unsigned)ctas), block(32 * kWarps);
     if (p.k_scale) {
-        if (p.head_dim == 128) accumulate_kernel<128, true><<<grid, block, 0, stream>>>(p);
-        else accumulate_kernel<64, true><<<grid, block, 0, stream>>>(p);
+        if (p.head_dim == 128) launch<128, true>(p, sm_count, stream);
+        else launch<64, true>(p, sm_count, stream);
     } else {
-        if (p.head_dim == 128) accumulate_kernel<128, false><<<grid, block, 0, stream>>>(p);
-        else accumulate_kernel<64, false><<<grid, block, 0, stream>>>(p);
+        if (p.head_dim == 128) launch<128, false>(p, sm_count, stream);
+        else launch<64, false>(p, sm_count, stream);
     }
     return cudaGetLastError();
 }

@@ -239,23 +239,26 @@ __device__ __forceinline__ bool soft_any(bool x) {
 // and the first `rows` rows: O^T times the row's 1 / sum (in `inv`), or zeros.
 template <int R, typename F>
 __device__ __forceinline__ void store_rows(uint32_t tm, bool any, int rows, const float *inv, F put) {
+#pragma unroll 1
     for (int d = 0; d < R / 128; ++d) {
-        for (int r0 = 0; r0 < rows; r0 += 32) {
-            uint32_t o[32];
-            if (any) tc05::tmem_ld32(tm + 64 * d + r0, o);
-            if (any && r0 + 32 <= rows) {
+#pragma unroll 1
+        for (int r0 = 0; r0 < rows; r0 += 16) {
+            uint32_t o[16];
+            if (any) tmem_ld16(tm + 64 * d + r0, o);
+            float v[16];
 #pragma unroll
-                for (int e = 0; e < 32; ++e) {
-                    const float w = inv[r0 + e];
-                    put(r0 + e, 128 * d, w > 0.f ? __uint_as_float(o[e]) * w : 0.f);
-                }
+            for (int e = 0; e < 16; ++e) {
+                const float w = inv[r0 + e];
+                v[e] = any && w > 0.f ? __uint_as_float(o[e]) * w : 0.f;
+            }
+            // (a branch a store costs three times the stores: only the last chunk pays it)
+            if (r0 + 16 <= rows) {
+#pragma unroll
+                for (int e = 0; e < 16; ++e) put(r0 + e, 128 * d, v[e]);
             } else {
 #pragma unroll
-                for (int e = 0; e < 32; ++e)
-                    if (r0 + e < rows) {
-                        const float w = inv[r0 + e];
-                        put(r0 + e, 128 * d, any && w > 0.f ? __uint_as_float(o[e]) * w : 0.f);
-                    }
+                for (int e = 0; e < 16; ++e)
+                    if (r0 + e < rows) put(r0 + e, 128 * d, v[e]);
             }
         }
     }
@@ -280,8 +283,8 @@ latent_kernel(const LatentParams p, const Partials part, const __grid_constant__
     const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
     const uint32_t sQ = base, sX = base + Sh::kQBytes, sP = sX + NS * Sh::kTileBytes;
     const uint32_t bars = smem_u32(bar_mem);
-    auto full = [&](int i) { return bars + 8u * i; };
-    auto empty = [&](int i) { return bars + 8u * (NS + i); };
+    auto full = [&](uint32_t i) { return bars + 8u * i; };
+    auto empty = [&](uint32_t i) { return bars + 8u * (NS + i); };
     const uint32_t q_full = bars + 8u * (2 * NS), q_empty = q_full + 8;
     auto s_full = [&](uint32_t i) { return q_full + 16 + 8 * i; };
     auto s_empty = [&](uint32_t i) { return q_full + 32 + 8 * i; };
@@ -289,10 +292,7 @@ latent_kernel(const LatentParams p, const Partials part, const __grid_constant__
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
 
     if (threadIdx.x == 0) {
-        for (int i = 0; i < NS; ++i) {
-            mbar_init(full(i), 1);
-            mbar_init(empty(i), 1);
-        }
+        for (int i = 0; i < 2 * NS; ++i) mbar_init(bars + 8 * i, 1);
         mbar_init(q_full, 1);
         mbar_init(q_empty, 1);
         for (int i = 0; i < 2; ++i) {
@@ -361,12 +361,13 @@ latent_kernel(const LatentParams p, const Partials part, const __grid_constant__
             if (s.tiles == 0) continue;
             // kAhead tiles beyond the ring are fetched into L2: HBM's latency then passes
             // under their predecessors' turns, and the ring's own loads come from L2
-            int grp[kAhead + 1];
+            // (and a tile's table entry is read one turn before that)
+            int grp[kAhead + 2];
 #pragma unroll
-            for (int k = 0; k < kAhead; ++k) grp[k] = k < s.tiles ? group_of(s.tile0 + k) : -1;
+            for (int k = 0; k <= kAhead; ++k) grp[k] = k < s.tiles ? group_of(s.tile0 + k) : -1;
             for (int i = 0; i < s.tiles; ++i, ++g) {
-                grp[kAhead] = i + kAhead < s.tiles ? group_of(s.tile0 + i + kAhead) : -1;
                 if (grp[kAhead] >= 0) prefetch_4d(&tmap_x, 0, 0, 0, grp[kAhead]);
+                grp[kAhead + 1] = i + kAhead + 1 < s.tiles ? group_of(s.tile0 + i + kAhead + 1) : -1;
                 const int t0 = (s.tile0 + i) * kN;
                 const int ntok = s.t_end - t0 < kN ? s.t_end - t0 : kN;
                 const int nbox = (ntok + 15) / 16;
@@ -395,7 +396,7 @@ latent_kernel(const LatentParams p, const Partials part, const __grid_constant__
                                 full(st));
                 __syncwarp();
 #pragma unroll
-                for (int k = 0; k < kAhead; ++k) grp[k] = grp[k + 1];
+                for (int k = 0; k <= kAhead; ++k) grp[k] = grp[k + 1];
             }
             ++nseg;
         }
@@ -420,8 +421,8 @@ latent_kernel(const LatentParams p, const Partials part, const __grid_constant__
             ok = warp_wait(q_full, nseg & 1);
             for (int i = 0; i < tiles && ok; ++i, ++g) {
                 const uint32_t st = g % NS, sb = g & 1;
-                ok = !__any_sync(0xffffffffu, abort_flag) && warp_wait(full(st), (g / NS) & 1) &&
-                     warp_wait(s_empty(sb), ((g >> 1) & 1) ^ 1);
+                ok = !__any_sync(0xffffffffu, abort_flag) && warp_wait(s_empty(sb), ((g >> 1) & 1) ^ 1) &&
+                     warp_wait(full(st), (g / NS) & 1);
                 if (!ok) break;
                 tc05::fence_after_sync();
                 const uint64_t xd = tc05::sdesc_sw128(sX + st * Sh::kTileBytes, 16, Sh::kGroupBytes);
@@ -459,6 +460,7 @@ latent_kernel(const LatentParams p, const Partials part, const __grid_constant__
                 tc05::fence_after_sync();
                 const uint64_t cd = tc05::sdesc_sw128(sX + st * Sh::kTileBytes, 1024, Sh::kGroupBytes);
                 if (elect_one()) {
+                    // (one accumulator after the other: alternating between them costs a fifth)
 #pragma unroll
                     for (int d = 0; d < Sh::kDimTiles; ++d)
 #pragma unroll
@@ -557,6 +559,7 @@ latent_kernel(const LatentParams p, const Partials part, const __grid_constant__
                 // gave up acted on) by all four warps together
                 const bool any = soft_any(need || fail);
                 // the P buffer is free, and O^T complete, once the previous value product is done
+                // (which overlaps with the maximum above)
                 if (g > 0 && !warp_wait(pv_done, (g - 1) & 1)) fail = true;
                 if (any) {
                     stop = soft_any(fail);
