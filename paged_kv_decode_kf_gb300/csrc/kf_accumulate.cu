@@ -92,28 +92,14 @@ struct Columns {
     int hide[2];
 
     template <bool KV8>
-    __device__ __forceinline__ void load(const AccumulateParams &p, const AccRequest &r, int h, int64_t c0, int64_t cols,
-                                         int log_g, float kscale) {
-        const int lane = threadIdx.x & 31, g = lane >> 2, t4 = lane & 3;
-        const int G = 1 << log_g;
-        const int64_t col = c0 + g;  // zeros past the last
-        const uint16_t *qrow = p.q + (((r.q0 + (col >> log_g)) * p.num_q_heads) + h * G + (col & (G - 1))) * D;
-#pragma unroll
-        for (int i = 0; i < NQ; ++i) {
-            // bf16 K: chunk t4 + 4 i of 8 numbers; E4M3 K: 16 numbers at 16 (t4 + 4 (i / 2))
-            const int e = KV8 ? 16 * (t4 + 4 * (i >> 1)) + 8 * (i & 1) : 8 * (t4 + 4 * i);
-            q[i] = col < cols ? __ldg(reinterpret_cast<const uint4 *>(qrow + e)) : make_uint4(0, 0, 0, 0);
-        }
+    __device__ __forceinline__ void ready(float scale_log2, float kscale) {
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
-            const int64_t cc = c0 + 2 * t4 + u;
-            float l = INFINITY;  // weight 0
-            if (cc < cols) l = p.lse[(r.q0 + (cc >> log_g)) * p.num_q_heads + h * G + (cc & (G - 1))];
-            lse2[u] = l == -INFINITY ? INFINITY : l * 1.4426950408889634f;
-            hide[u] = (int)(p.causal ? r.shift + (cc >> log_g) : r.L);  // (lengths are 32-bit)
-            c[u] = p.scale_log2;
+            lse2[u] = lse2[u] == -INFINITY ? INFINITY : lse2[u] * 1.4426950408889634f;
+            c[u] = scale_log2;
         }
         if (KV8) {
+            const int t4 = threadIdx.x & 3;
             float mx = 0.f;
 #pragma unroll
             for (int i = 0; i < NQ; ++i) {
@@ -142,39 +128,119 @@ struct Columns {
     }
 };
 
+// Where a lane's columns lie, from column c0 on; `step` columns further at a time.
+template <int D, bool KV8>
+struct ColumnWalk {
+    const uint16_t *q;       // row of column c0 + g, from this lane's part on
+    const float *lse[2];     // of columns c0 + 2 t4 and + 1
+    int64_t q_stride, lse_stride;
+    int hide[2], hide_stride;
+    int left;                // columns from c0 on
+
+    __device__ __forceinline__ ColumnWalk(const AccumulateParams &p, const AccRequest &r, int h, int64_t c0,
+                                          int64_t cols, int step, int log_g) {
+        const int lane = threadIdx.x & 31, g = lane >> 2, t4 = lane & 3;
+        const int G = 1 << log_g;
+        const int64_t col = c0 + g;
+        // bf16 K: chunk t4 + 4 i of 8 numbers; E4M3 K: 16 numbers at 16 (t4 + 4 (i / 2))
+        q = p.q + (((r.q0 + (col >> log_g)) * p.num_q_heads) + h * G + (col & (G - 1))) * D + (KV8 ? 16 : 8) * t4;
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+            const int64_t cc = c0 + 2 * t4 + u;
+            lse[u] = p.lse + (r.q0 + (cc >> log_g)) * p.num_q_heads + h * G + (cc & (G - 1));
+            hide[u] = (int)(p.causal ? r.shift + (cc >> log_g) : r.L);  // (lengths are 32-bit)
+        }
+        // (step is a multiple of 8, and so of G)
+        lse_stride = (int64_t)(step >> log_g) * p.num_q_heads;
+        q_stride = lse_stride * D;
+        hide_stride = p.causal ? step >> log_g : 0;
+        left = (int)(cols - c0);
+    }
+
+    // Asks for eight columns (zeros, and no weight, past the last); Columns::ready
+    // makes them fragments. What lies between the two hides the loads.
+    __device__ __forceinline__ void load(Columns<D> &x) const {
+        const int lane = threadIdx.x & 31, g = lane >> 2, t4 = lane & 3;
+#pragma unroll
+        for (int i = 0; i < Columns<D>::NQ; ++i) {
+            const int e = KV8 ? 64 * (i >> 1) + 8 * (i & 1) : 32 * i;
+            x.q[i] = g < left ? __ldg(reinterpret_cast<const uint4 *>(q + e)) : make_uint4(0, 0, 0, 0);
+        }
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+            x.lse2[u] = 2 * t4 + u < left ? __ldg(lse[u]) : INFINITY;
+            x.hide[u] = hide[u];
+        }
+    }
+
+    __device__ __forceinline__ bool next(int step) {
+        left -= step;
+        q += q_stride;
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+            lse[u] += lse_stride;
+            hide[u] += hide_stride;
+        }
+        return left > 0;
+    }
+};
+
 // sum[k][w] += the weights the eight columns give the tokens t0 + 16 k + g + 8 w.
 template <int D, bool KV8, int T>
 __device__ __forceinline__ void add_columns(const uint4 (&kr)[T][2][KV8 ? D / 64 : D / 32], const Columns<D> &q,
                                             int t0, float (&sum)[T][2]) {
     const int g = (threadIdx.x & 31) >> 2;
+    float s[T][4];
 #pragma unroll
-    for (int k = 0; k < T; ++k) {
-        float s[4] = {0.f, 0.f, 0.f, 0.f};
+    for (int k = 0; k < T; ++k) s[k][0] = s[k][1] = s[k][2] = s[k][3] = 0.f;
+    // (tiles innermost: T independent chains of products)
 #pragma unroll
-        for (int i = 0; i < (KV8 ? D / 64 : D / 32); ++i) {
-            const uint4 ka = kr[k][0][i], kb = kr[k][1][i];
-            if (KV8) {
-                const uint32_t wa[4] = {ka.x, ka.y, ka.z, ka.w}, wb[4] = {kb.x, kb.y, kb.z, kb.w};
+    for (int i = 0; i < (KV8 ? D / 64 : D / 32); ++i) {
+        if (KV8) {
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const uint32_t a[4] = {e4m3x2_to_f16x2(wa[e]), e4m3x2_to_f16x2(wb[e]),
-                                           e4m3x2_to_f16x2(wa[e] >> 16), e4m3x2_to_f16x2(wb[e] >> 16)};
-                    const uint4 qq = q.q[(2 * i + (e >> 1)) % (D / 32)];
-                    if (e & 1) mma_f16(s, a, qq.z, qq.w);
-                    else mma_f16(s, a, qq.x, qq.y);
+            for (int e = 0; e < 4; ++e) {
+                const uint4 qq = q.q[(2 * i + (e >> 1)) % (D / 32)];
+#pragma unroll
+                for (int k = 0; k < T; ++k) {
+                    const uint4 ka = kr[k][0][i], kb = kr[k][1][i];
+                    const uint32_t wa = e == 0 ? ka.x : e == 1 ? ka.y : e == 2 ? ka.z : ka.w;
+                    const uint32_t wb = e == 0 ? kb.x : e == 1 ? kb.y : e == 2 ? kb.z : kb.w;
+                    const uint32_t a[4] = {e4m3x2_to_f16x2(wa), e4m3x2_to_f16x2(wb), e4m3x2_to_f16x2(wa >> 16),
+                                           e4m3x2_to_f16x2(wb >> 16)};
+                    if (e & 1) mma_f16(s[k], a, qq.z, qq.w);
+                    else mma_f16(s[k], a, qq.x, qq.y);
                 }
-            } else {
-                const uint32_t a0[4] = {ka.x, kb.x, ka.y, kb.y}, a1[4] = {ka.z, kb.z, ka.w, kb.w};
-                mma_bf16(s, a0, q.q[i].x, q.q[i].y);
-                mma_bf16(s, a1, q.q[i].z, q.q[i].w);
+            }
+        } else {
+#pragma unroll
+            for (int k = 0; k < T; ++k) {
+                const uint32_t a[4] = {kr[k][0][i].x, kr[k][1][i].x, kr[k][0][i].y, kr[k][1][i].y};
+                mma_bf16(s[k], a, q.q[i].x, q.q[i].y);
+            }
+#pragma unroll
+            for (int k = 0; k < T; ++k) {
+                const uint32_t a[4] = {kr[k][0][i].z, kr[k][1][i].z, kr[k][0][i].w, kr[k][1][i].w};
+                mma_bf16(s[k], a, q.q[i].z, q.q[i].w);
             }
         }
-        const int t = t0 + 16 * k + g;
+    }
+    // (the newest token of a window hides from the older queries: a few runs only)
+    if (__all_sync(0xffffffffu, t0 + 16 * T - 1 <= min(q.hide[0], q.hide[1]))) {
 #pragma unroll
-        for (int u = 0; u < 2; ++u)
+        for (int k = 0; k < T; ++k)
 #pragma unroll
             for (int w = 0; w < 2; ++w)
-                if (t + 8 * w <= q.hide[u]) sum[k][w] += exp2_approx(fmaf(s[2 * w + u], q.c[u], -q.lse2[u]));
+                sum[k][w] += exp2_approx(fmaf(s[k][2 * w], q.c[0], -q.lse2[0])) +
+                             exp2_approx(fmaf(s[k][2 * w + 1], q.c[1], -q.lse2[1]));
+    } else {
+#pragma unroll
+        for (int k = 0; k < T; ++k)
+#pragma unroll
+            for (int w = 0; w < 2; ++w)
+#pragma unroll
+                for (int u = 0; u < 2; ++u)
+                    if (t0 + 16 * k + g + 8 * w <= q.hide[u])
+                        sum[k][w] += exp2_approx(fmaf(s[k][2 * w + u], q.c[u], -q.lse2[u]));
     }
 }
 
@@ -186,13 +252,13 @@ __device__ __forceinline__ void key_rows(const AccumulateParams &p, int b, int64
     const int lane = threadIdx.x & 31, g = lane >> 2, t4 = lane & 3;
 #pragma unroll
     for (int k = 0; k < T; ++k) {
-        const int64_t t = (tile0 + (k < tiles ? k : tiles - 1)) * 16;
-        int64_t phys = p.block_tables[(int64_t)b * p.bt_stride + t / p.block_size];
+        const int t = (int)(tile0 + (k < tiles ? k : tiles - 1)) * 16;
+        int64_t phys = p.block_tables[(int64_t)b * p.bt_stride + (t >> block_shift(p.block_size))];
         if (phys < 0 || phys >= p.num_blocks) {
             if (lane == 0) raise_error(p.err, KF_DEVERR_BLOCK_ID);
             phys = 0;
         }
-        const int64_t first = phys * p.block_size + t % p.block_size;
+        const int64_t first = phys * p.block_size + (t & (p.block_size - 1));
 #pragma unroll
         for (int u = 0; u < 2; ++u)
             row[k][u] = static_cast<const uint8_t *>(p.k_cache) +
@@ -254,11 +320,13 @@ accumulate_kernel(const AccumulateParams p) {
                     for (int i = 0; i < NL; ++i)
                         kr[k][u][i] = load_stream(row[k][u] + (int64_t)h * (D * EB) + i * 64);
             const float kscale = KV8 ? p.k_scale[h] : 1.f;
-            for (int64_t c0 = col0; c0 < cols; c0 += 8) {
+            ColumnWalk<D, KV8> walk(p, r, h, col0, cols, 8, log_g);
+            do {
                 Columns<D> q;
-                q.template load<KV8>(p, r, h, c0, cols, log_g, kscale);
+                walk.load(q);
+                q.template ready<KV8>(p.scale_log2, kscale);
                 add_columns<D, KV8, kTiles>(kr, q, (int)tile0 * 16, sum);
-            }
+            } while (walk.next(8));
         }
 #pragma unroll
         for (int k = 0; k < kTiles; ++k) {
@@ -322,13 +390,14 @@ accumulate_window_kernel(const AccumulateParams p) {
         // with a causal window, columns of queries before the first that sees this run add nothing
         int64_t col0 = 0;
         if (p.causal && t0 > r.shift) col0 = ((t0 - r.shift) << log_g) & ~7ll;
-        const int64_t step = 8 * share;
+        const int step = 8 * share;
         for (int h = warp / share; h < heads; h += kWinWarps) {
             int64_t c0 = col0 + 8 * (warp % share);
             if (c0 >= cols) continue;
             const float kscale = KV8 ? p.k_scale[h] : 1.f;
+            ColumnWalk<D, KV8> walk(p, r, h, c0, cols, step, log_g);
             Columns<D> q;
-            q.template load<KV8>(p, r, h, c0, cols, log_g, kscale);
+            walk.load(q);
             uint4 kr[kWinTiles][2][NL];
 #pragma unroll
             for (int k = 0; k < kWinTiles; ++k)
@@ -338,12 +407,12 @@ accumulate_window_kernel(const AccumulateParams p) {
                     for (int i = 0; i < NL; ++i) kr[k][u][i] = load_stream(row[k][u] + (int64_t)h * (D * EB) + i * 64);
             while (true) {
                 Columns<D> next;
-                const bool more = c0 + step < cols;
-                if (more) next.template load<KV8>(p, r, h, c0 + step, cols, log_g, kscale);
+                q.template ready<KV8>(p.scale_log2, kscale);
+                const bool more = walk.next(step);
+                if (more) walk.load(next);
                 add_columns<D, KV8, kWinTiles>(kr, q, (int)t0, sum);
                 if (!more) break;
                 q = next;
-                c0 += step;
             }
         }
 #pragma unroll
