@@ -51,36 +51,6 @@ __device__ __forceinline__ float exp2_approx(float x) {
     return y;
 }
 
-struct AccRequest {
-    int64_t q0, C, L, shift;  // query j < C sees tokens t <= shift + j (causal)
-};
-
-__device__ __forceinline__ AccRequest acc_request(const AccumulateParams &p, int b, bool report) {
-    int64_t q0 = b, q1 = b + 1;
-    if (p.q_start) {
-        q0 = p.q_start[b];
-        q1 = p.q_start[b + 1];
-    }
-    if (q0 < 0 || q1 < q0 || q1 > p.num_q_tokens) {
-        if (report) raise_error(p.err, KF_DEVERR_CONTEXT_LEN);
-        return {0, 0, 0, 0};
-    }
-    AccRequest r;
-    r.q0 = q0;
-    r.C = q1 - q0;
-    int64_t L = p.ctx_lens[b];
-    const int64_t cap = (int64_t)p.bt_stride * p.block_size;
-    if (L < 0 || L > cap) {
-        if (report) raise_error(p.err, KF_DEVERR_CONTEXT_LEN);
-        L = L < 0 ? 0 : cap;
-    }
-    r.shift = L - r.C;
-    if ((L > p.max_context_len || r.C > p.max_query_len) && report) raise_error(p.err, KF_DEVERR_MAX_CONTEXT);
-    r.L = L < p.max_context_len ? L : p.max_context_len;
-    if (r.C > p.max_query_len) r.C = p.max_query_len;
-    return r;
-}
-
 // Eight columns (j, g) of one KV head as B fragments: lane (g, t4) holds part t4 of
 // column c0 + g; and of its two result columns 2 t4, 2 t4 + 1 the lse, the scale
 // and the last token they see.
@@ -346,17 +316,18 @@ accumulate_kernel(const AccumulateParams p) {
     }
 }
 
-// Windows of queries (more than eight columns a KV head): one CTA a run of 64 tokens,
+// Windows of queries (more than eight columns a KV head) over E4M3 keys: one CTA a run of 64 tokens,
 // its eight warps split the (KV head, column group) pairs, so that the tokens' keys
 // are held while the columns pass (128 registers at D = 128) and q, which every CTA
 // reads whole, is read once per 64 tokens. The next group's q is asked for before this
 // one's products. The warps' sums meet in shared memory, in warp order.
 constexpr int kWinWarps = 8, kWinTiles = 4;
 
-template <int D, bool KV8>
+template <int D>
 __global__ void __launch_bounds__(32 * kWinWarps, 1)
 accumulate_window_kernel(const AccumulateParams p) {
-    constexpr int NL = KV8 ? D / 64 : D / 32, EB = KV8 ? 1 : 2;
+    constexpr bool KV8 = true;
+    constexpr int NL = D / 64, EB = 1;
     __shared__ int64_t sm_loc[36];
     __shared__ float part[kWinWarps][kWinTiles * 16];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -394,7 +365,7 @@ accumulate_window_kernel(const AccumulateParams p) {
         for (int h = warp / share; h < heads; h += kWinWarps) {
             int64_t c0 = col0 + 8 * (warp % share);
             if (c0 >= cols) continue;
-            const float kscale = KV8 ? p.k_scale[h] : 1.f;
+            const float kscale = p.k_scale[h];
             ColumnWalk<D, KV8> walk(p, r, h, c0, cols, step, log_g);
             Columns<D> q;
             walk.load(q);
@@ -438,10 +409,12 @@ accumulate_window_kernel(const AccumulateParams p) {
 }
 
 template <int D, bool KV8>
-void launch(const AccumulateParams &p, int sm_count, cudaStream_t stream) {
-    // Columns a KV head: up to eight are one pass of the row kernel (96 us on 64
-    // requests of 4K with one query); more keep the keys while the columns pass.
+cudaError_t launch(const AccumulateParams &p, int sm_count, cudaStream_t stream, void *encode_fn) {
+    // Columns a KV head: up to eight are one pass of the row kernel; more keep the keys
+    // while the columns pass, bf16 ones on tcgen05 (E4M3 keys need fp16 products, and
+    // tcgen05 takes no fp16 operand beside an 8-bit one).
     const int64_t cols = (int64_t)p.max_query_len * (p.num_q_heads / p.num_kv_heads);
+    if (!KV8 && cols > 8 && p.num_q_tokens > 0) return launch_accumulate_tc05(p, sm_count, stream, encode_fn);
     const int64_t tiles = (int64_t)p.batch * ((p.max_context_len + 15) / 16);
     // one wave of resident CTAs, no more warps (CTAs) than the batch can have tiles (runs)
     if (cols <= 8) {
@@ -449,22 +422,19 @@ void launch(const AccumulateParams &p, int sm_count, cudaStream_t stream) {
         accumulate_kernel<D, KV8><<<(unsigned)ctas, 32 * kWarps, 0, stream>>>(p);
     } else {
         const int64_t runs = (int64_t)p.batch * ((p.max_context_len + 16 * kWinTiles - 1) / (16 * kWinTiles));
-        accumulate_window_kernel<D, KV8>
-            <<<(unsigned)(runs < sm_count ? runs : sm_count), 32 * kWinWarps, 0, stream>>>(p);
+        accumulate_window_kernel<D><<<(unsigned)(runs < sm_count ? runs : sm_count), 32 * kWinWarps, 0, stream>>>(p);
     }
+    return cudaGetLastError();
 }
 
 }  // namespace
 
-cudaError_t launch_accumulate(const AccumulateParams &p, int sm_count, cudaStream_t stream) {
-    if (p.k_scale) {
-        if (p.head_dim == 128) launch<128, true>(p, sm_count, stream);
-        else launch<64, true>(p, sm_count, stream);
-    } else {
-        if (p.head_dim == 128) launch<128, false>(p, sm_count, stream);
-        else launch<64, false>(p, sm_count, stream);
-    }
-    return cudaGetLastError();
+cudaError_t launch_accumulate(const AccumulateParams &p, int sm_count, cudaStream_t stream, void *encode_fn) {
+    if (p.k_scale)
+        return p.head_dim == 128 ? launch<128, true>(p, sm_count, stream, encode_fn)
+                                 : launch<64, true>(p, sm_count, stream, encode_fn);
+    return p.head_dim == 128 ? launch<128, false>(p, sm_count, stream, encode_fn)
+                             : launch<64, false>(p, sm_count, stream, encode_fn);
 }
 
 }  // namespace kf

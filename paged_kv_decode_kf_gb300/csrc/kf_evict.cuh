@@ -23,7 +23,39 @@ struct AccumulateParams {
     float scale_log2;
 };
 
-cudaError_t launch_accumulate(const AccumulateParams &p, int sm_count, cudaStream_t stream);
+struct AccRequest {
+    int64_t q0, C, L, shift;  // query j < C sees tokens t <= shift + j (causal)
+};
+
+__device__ __forceinline__ AccRequest acc_request(const AccumulateParams &p, int b, bool report) {
+    int64_t q0 = b, q1 = b + 1;
+    if (p.q_start) {
+        q0 = p.q_start[b];
+        q1 = p.q_start[b + 1];
+    }
+    if (q0 < 0 || q1 < q0 || q1 > p.num_q_tokens) {
+        if (report) raise_error(p.err, KF_DEVERR_CONTEXT_LEN);
+        return {0, 0, 0, 0};
+    }
+    AccRequest r;
+    r.q0 = q0;
+    r.C = q1 - q0;
+    int64_t L = p.ctx_lens[b];
+    const int64_t cap = (int64_t)p.bt_stride * p.block_size;
+    if (L < 0 || L > cap) {
+        if (report) raise_error(p.err, KF_DEVERR_CONTEXT_LEN);
+        L = L < 0 ? 0 : cap;
+    }
+    r.shift = L - r.C;
+    if ((L > p.max_context_len || r.C > p.max_query_len) && report) raise_error(p.err, KF_DEVERR_MAX_CONTEXT);
+    r.L = L < p.max_context_len ? L : p.max_context_len;
+    if (r.C > p.max_query_len) r.C = p.max_query_len;
+    return r;
+}
+
+cudaError_t launch_accumulate(const AccumulateParams &p, int sm_count, cudaStream_t stream, void *encode_fn);
+// bf16 keys and more than eight (query, head) columns a KV head.
+cudaError_t launch_accumulate_tc05(const AccumulateParams &p, int sm_count, cudaStream_t stream, void *encode_fn);
 
 struct EvictParams {
     uint4 *cache_a, *cache_b;     // [NB, bs] rows of row_vecs 16-byte vectors; cache_b may be null

@@ -117,7 +117,9 @@ kf_status accumulate_impl(const void *q, const int32_t *q_start, const void *k_c
     p.block_size = block_size;
     p.causal = causal;
     p.scale_log2 = scale * kLog2e;
-    return from_launch(launch_accumulate(p, sms, reinterpret_cast<cudaStream_t>(stream)));
+    void *fn = tensor_map_encoder();
+    if (!fn) return KF_ERR_CUDA;
+    return from_launch(launch_accumulate(p, sms, reinterpret_cast<cudaStream_t>(stream), fn));
 }
 
 // Rows that can move: into slots below `keep`, from indices at or above it.
