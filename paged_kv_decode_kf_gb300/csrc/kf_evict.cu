@@ -39,12 +39,17 @@ struct Keys {
     int64_t sink, recent_from;  // protected: position < sink or >= recent_from
 
     __device__ __forceinline__ uint32_t operator()(int64_t t) const {
-        const int64_t pos = positions ? positions[t] : t;
-        if (pos < sink || pos >= recent_from) return 0xffffffffu;
-        const float s = scores[t];
+        return of(scores[t], positions ? positions[t] : t);
+    }
+
+    __device__ __forceinline__ static uint32_t rank_of(float s) {
         if (s != s) return 0u;
         const uint32_t u = __float_as_uint(s == 0.f ? 0.f : s);
         return (u >> 31) ? ~u : (u | 0x80000000u);
+    }
+
+    __device__ __forceinline__ uint32_t of(float s, int64_t pos) const {
+        return pos < sink || pos >= recent_from ? 0xffffffffu : rank_of(s);
     }
 };
 
@@ -71,28 +76,19 @@ __device__ __forceinline__ int remote(const int *p, int rank) {
     return v;
 }
 
-// Exclusive prefix sum of `x` over the block.
-__device__ __forceinline__ int block_scan(int x, int *warp_sums, int &total) {
+// Exclusive prefix sum over the block's 32 warps of `x` (one value a warp).
+__device__ __forceinline__ int warp_scan(int x, int *sums, int &total) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    int v = x;
-    for (int o = 1; o < 32; o <<= 1) {
-        const int y = __shfl_up_sync(0xffffffffu, v, o);
-        if (lane >= o) v += y;
-    }
-    __syncthreads();  // warp_sums is free again
-    if (lane == 31) warp_sums[warp] = v;
+    __syncthreads();  // `sums` is free again
+    if (lane == 0) sums[warp] = x;
     __syncthreads();
-    int before = 0, all = 0;
-    {
-        int w = warp_sums[lane];
-        all = w;
-        for (int o = 16; o; o >>= 1) all += __shfl_xor_sync(0xffffffffu, all, o);
-        w = lane < warp ? w : 0;
-        for (int o = 16; o; o >>= 1) w += __shfl_xor_sync(0xffffffffu, w, o);
-        before = w;
+    int all = sums[lane], before = lane < warp ? all : 0;
+    for (int o = 16; o; o >>= 1) {
+        all += __shfl_xor_sync(0xffffffffu, all, o);
+        before += __shfl_xor_sync(0xffffffffu, before, o);
     }
     total = all;
-    return v - x + before;
+    return before;
 }
 
 __device__ __forceinline__ void move_row(const EvictParams &p, int b, int src, int dst, int lane) {
@@ -135,9 +131,10 @@ __global__ void __launch_bounds__(kSelThreads)
 evict_select_kernel(const EvictParams p, int key_slots) {
     __shared__ int hist[256 * kCopies];
     __shared__ int sums[2][256];  // this CTA's histogram, double-buffered over passes
-    __shared__ int warp_sums[32];
+    __shared__ int warp_sums[64];
     __shared__ int s_digit, s_left;
     __shared__ int s_counts[2];   // this CTA's holes and movers
+    __shared__ int s_before[3], all_bins[CL > 1 ? 256 : 1];
     extern __shared__ uint32_t keys[];
     const int b = blockIdx.x / CL, tid = threadIdx.x;
     const int rank = CL == 1 ? 0 : (int)cluster_rank();
@@ -161,10 +158,29 @@ evict_select_kernel(const EvictParams p, int key_slots) {
     const int keep = p.keep;
     const int per = (L + CL - 1) / CL;                 // this CTA's tokens: [lo, hi)
     const int lo = min(rank * per, L), hi = min(lo + per, L);
-    // what stays below `keep` keeps its score and position (movers come after)
-    for (int t = lo + tid; t < min(hi, keep); t += kSelThreads) {
-        scores_out[t] = scores[t];
-        if (positions) positions_out[t] = positions[t];
+    const bool cached = per <= key_slots && L > keep;
+    const Keys key{scores, positions, p.sink, (positions ? (int64_t)p.seq_lens[b] : (int64_t)L) - p.recent};
+    // one read of scores and positions: below `keep` they keep their place (movers come
+    // after), and the keys go to shared memory
+    const int end = cached ? hi : min(hi, keep);
+    for (int t0 = lo + tid; t0 < end; t0 += 4 * kSelThreads) {
+        float sc[4];
+        int32_t pos[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int t = t0 + i * kSelThreads;
+            sc[i] = t < end ? scores[t] : 0.f;
+            pos[i] = positions && t < end ? positions[t] : t;
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int t = t0 + i * kSelThreads;
+            if (t < min(end, keep)) {
+                scores_out[t] = sc[i];
+                if (positions) positions_out[t] = pos[i];
+            }
+            if (cached && t < end) keys[t - lo] = key.of(sc[i], pos[i]);
+        }
     }
     if (L <= keep) {
         if (report) {
@@ -173,10 +189,6 @@ evict_select_kernel(const EvictParams p, int key_slots) {
         }
         return;
     }
-    const Keys key{scores, positions, p.sink, (positions ? (int64_t)p.seq_lens[b] : (int64_t)L) - p.recent};
-    const bool cached = per <= key_slots;
-    if (cached)
-        for (int t = lo + tid; t < hi; t += kSelThreads) keys[t - lo] = key(t);
     auto key_at = [&](int t) { return cached ? keys[t - lo] : key(t); };
 
     // the keep-th largest key, from its highest byte down
@@ -201,14 +213,25 @@ evict_select_kernel(const EvictParams p, int key_slots) {
             mine[tid] = n;
         }
         cluster_sync<CL>();
+        const int *bins = mine;
+        if (CL > 1) {  // a bin a thread, all ranks' loads in flight at once
+            if (tid < 256) {
+                int v[CL], n = 0;
+#pragma unroll
+                for (int r = 0; r < CL; ++r) v[r] = remote<CL>(&mine[tid], r);
+#pragma unroll
+                for (int r = 0; r < CL; ++r) n += v[r];
+                all_bins[tid] = n;
+            }
+            __syncthreads();
+            bins = all_bins;
+        }
         // warp 0 finds the digit: lane l holds bins 255 - 8 l down to 248 - 8 l
         if (tid < 32) {
             int bin[8], n = 0;
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                bin[i] = 0;
-#pragma unroll
-                for (int r = 0; r < CL; ++r) bin[i] += remote<CL>(&mine[255 - 8 * tid - i], r);
+                bin[i] = bins[255 - 8 * tid - i];
                 n += bin[i];
             }
             int above = n;  // inclusive sum from the largest digit down
@@ -231,56 +254,75 @@ evict_select_kernel(const EvictParams p, int key_slots) {
         __syncthreads();
         prefix |= (uint32_t)s_digit << shift;
         left = s_left;
-        if (pass == 3)
-            for (int r = 0; r < rank; ++r) eq_before += remote<CL>(&mine[prefix & 255], r);
+    }
+    // keys equal to the last kept one in the CTAs before this: lane r asks CTA r
+    if (CL > 1) {
+        if (tid < 32) {
+            int n = tid < rank ? remote<CL>(&sums[1][prefix & 255], tid) : 0;
+            for (int o = 16; o; o >>= 1) n += __shfl_xor_sync(0xffffffffu, n, o);
+            if (tid == 0) s_before[2] = n;
+        }
+        __syncthreads();
+        eq_before = s_before[2];
     }
 
-    // which tokens stay: each thread takes a run of this CTA's tokens, in order
-    // (an odd length: neighbours' reads fall into different banks)
-    const int len = ((per + kSelThreads - 1) / kSelThreads) | 1;
-    const int t0 = min(lo + tid * len, hi), t1 = min(t0 + len, hi);
+    // which tokens stay: each warp takes a run of this CTA's tokens, 32 at a time in order
+    const int lane = tid & 31, warp = tid >> 5;
+    const int len = (((per + 31) / 32) + 31) & ~31;
+    const int t0 = min(lo + warp * len, hi), t1 = min(t0 + len, hi);
+    const uint32_t below = (1u << lane) - 1;
     int eq = 0;
-    for (int t = t0; t < t1; ++t) eq += key_at(t) == prefix;
+    for (int t = t0 + lane; t - lane < t1; t += 32) eq += __popc(__ballot_sync(0xffffffffu, t < t1 && key_at(t) == prefix));
     int total;
-    const int eq_rank = eq_before + block_scan(eq, warp_sums, total);
-    int holes = 0, movers = 0;
-    {
+    const int eq_rank = eq_before + warp_scan(eq, warp_sums, total);
+    // fn(token, hole, mover) for each of the warp's tokens, whole warps at a time
+    auto each = [&](auto &&fn) {
         int e = eq_rank;
-        for (int t = t0; t < t1; ++t) {
-            const uint32_t k = key_at(t);
-            const bool kept = k > prefix || (k == prefix && e++ < left);
-            holes += t < keep && !kept;
-            movers += t >= keep && kept;
+        for (int t = t0 + lane; t - lane < t1; t += 32) {
+            const uint32_t k = t < t1 ? key_at(t) : 0u;
+            const bool same = t < t1 && k == prefix;
+            const uint32_t m = __ballot_sync(0xffffffffu, same);
+            const bool kept = t < t1 && (k > prefix || (same && e + __popc(m & below) < left));
+            e += __popc(m);
+            fn(t, t < t1 && t < keep && !kept, kept && t >= keep);
         }
-    }
+    };
+    int holes = 0, movers = 0;
+    each([&](int t, bool hole, bool mover) {
+        holes += __popc(__ballot_sync(0xffffffffu, hole));
+        movers += __popc(__ballot_sync(0xffffffffu, mover));
+    });
     int all_holes, all_movers;
-    int hole_at = block_scan(holes, warp_sums, all_holes), mover_at = block_scan(movers, warp_sums, all_movers);
+    int hole_at = warp_scan(holes, warp_sums, all_holes), mover_at = warp_scan(movers, warp_sums + 32, all_movers);
     if (CL > 1) {
         if (tid == 0) {
             s_counts[0] = all_holes;
             s_counts[1] = all_movers;
         }
         cluster_sync<CL>();
-        all_movers = 0;
-        for (int r = 0; r < CL; ++r) {
-            const int m = remote<CL>(&s_counts[1], r);
-            if (r < rank) {
-                hole_at += remote<CL>(&s_counts[0], r);
-                mover_at += m;
+        if (tid < 32) {
+            const int h = tid < rank ? remote<CL>(&s_counts[0], tid) : 0;
+            const int m = tid < CL ? remote<CL>(&s_counts[1], tid) : 0;
+            int before[3] = {h, tid < rank ? m : 0, m};
+#pragma unroll
+            for (int i = 0; i < 3; ++i) {
+                for (int o = 16; o; o >>= 1) before[i] += __shfl_xor_sync(0xffffffffu, before[i], o);
+                if (tid == 0) s_before[i] = before[i];
             }
-            all_movers += m;
         }
+        __syncthreads();
+        hole_at += s_before[0];
+        mover_at += s_before[1];
+        all_movers = s_before[2];
     }
     int *dst = p.dst + (int64_t)b * p.max_moves, *src = p.src + (int64_t)b * p.max_moves;
-    {
-        int e = eq_rank;
-        for (int t = t0; t < t1; ++t) {
-            const uint32_t k = key_at(t);
-            const bool kept = k > prefix || (k == prefix && e++ < left);
-            if (t < keep && !kept) dst[hole_at++] = t;
-            if (t >= keep && kept) src[mover_at++] = t;
-        }
-    }
+    each([&](int t, bool hole, bool mover) {
+        const uint32_t h = __ballot_sync(0xffffffffu, hole), m = __ballot_sync(0xffffffffu, mover);
+        if (hole) dst[hole_at + __popc(h & below)] = t;
+        if (mover) src[mover_at + __popc(m & below)] = t;
+        hole_at += __popc(h);
+        mover_at += __popc(m);
+    });
     if (report) {
         p.counts[b] = all_movers;
         p.ctx_out[b] = keep;
@@ -290,18 +332,20 @@ evict_select_kernel(const EvictParams p, int key_slots) {
         scores_out[dst[i]] = scores[src[i]];
         if (positions) positions_out[dst[i]] = positions[src[i]];
     }
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     if (MOVE)
         for (int i = rank * (kSelThreads / 32) + (tid >> 5); i < all_movers; i += CL * (kSelThreads / 32))
             move_row(p, b, src[i], dst[i], tid & 31);
 }
 
-// One warp a moved row.
+// One warp a moved row at a time. The grid is set up while the selection ends.
 __global__ void __launch_bounds__(256)
 evict_move_kernel(const EvictParams p) {
-    const int b = blockIdx.y;
-    const int i = blockIdx.x * 8 + (threadIdx.x >> 5);
-    if (i >= p.counts[b]) return;
-    move_row(p, b, p.src[(int64_t)b * p.max_moves + i], p.dst[(int64_t)b * p.max_moves + i], threadIdx.x & 31);
+    asm volatile("griddepcontrol.wait;" ::: "memory");  // the lists are there
+    const int b = blockIdx.y, n = p.counts[b];
+    const int *src = p.src + (int64_t)b * p.max_moves, *dst = p.dst + (int64_t)b * p.max_moves;
+    for (int i = blockIdx.x * 8 + (threadIdx.x >> 5); i < n; i += gridDim.x * 8)
+        move_row(p, b, src[i], dst[i], threadIdx.x & 31);
 }
 
 template <int CL, bool MOVE>
@@ -344,8 +388,18 @@ cudaError_t launch_evict(const EvictParams &p, int sm_count, cudaStream_t stream
     if (in_place) e = wide ? launch_select<8, true>(p, stream) : launch_select<1, true>(p, stream);
     else e = wide ? launch_select<8, false>(p, stream) : launch_select<1, false>(p, stream);
     if (e != cudaSuccess || in_place) return e;
-    evict_move_kernel<<<dim3((p.max_moves + 7) / 8, p.batch), 256, 0, stream>>>(p);
-    return cudaGetLastError();
+    // at most some 4800 CTAs over the batch (a CTA for every eight possible moves was
+    // 10000 CTAs, most of them empty, where 33 requests moved 300 rows each)
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(std::min((p.max_moves + 7) / 8, std::max(1, 32 * sm_count / p.batch)), p.batch);
+    cfg.blockDim = dim3(256);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, evict_move_kernel, p);
 }
 
 }  // namespace kf
