@@ -15,6 +15,9 @@ __global__ void __launch_bounds__(128)
 append_latent_kernel(const uint4 *__restrict__ rows, const int32_t *__restrict__ row_start, uint4 *__restrict__ cache,
                      const int32_t *__restrict__ block_tables, int bt_stride, const int32_t *__restrict__ ctx_before,
                      int batch, int num_rows, int row_vecs, int block_size, int64_t num_blocks, unsigned int *err) {
+    // (an attention kernel that follows sets itself up meanwhile, and waits for this one
+    // before it reads anything)
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const int64_t row = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);
     const int lane = threadIdx.x & 31;
     if (row >= num_rows) return;

@@ -317,6 +317,7 @@ expand_kernel(const LatentParams p, const ExpandedKV kv, const __grid_constant__
         } while (w.step(p, fresh));
         if (range) raise_error(p.err, KF_DEVERR_RANGE);
     }
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the attention may be set up
     tc05::fence_before_sync();
     __syncthreads();
     if (warp == kIssuerWarp) {

@@ -125,6 +125,9 @@ expanded_kernel(const LatentParams p, const ExpandedKV kv, int q_tiles, const __
         return;
     }
     const int ntiles = (int)((t_end + kTok - 1) / kTok);
+    // the expansion's keys and values are complete from here on (its inputs, which this
+    // kernel read above, were so before it started)
+    asm volatile("griddepcontrol.wait;" ::: "memory");
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < NS; ++i) {
@@ -417,7 +420,8 @@ bool encode_q_rope(tc::EncodeFn fn, CUtensorMap *map, const LatentParams &p, int
 }
 
 template <int DN, int DV>
-cudaError_t launch(const LatentParams &p, const ExpandedKV &kv, cudaStream_t stream, tc::EncodeFn fn) {
+cudaError_t launch(const LatentParams &p, const ExpandedKV &kv, bool behind_expand, cudaStream_t stream,
+                   tc::EncodeFn fn) {
     using Sh = EShape<DN, DV>;
     const int64_t rows = (int64_t)p.num_heads * kv.rows;
     CUtensorMap mq, mk, mv, mr;
@@ -436,9 +440,17 @@ cudaError_t launch(const LatentParams &p, const ExpandedKV &kv, cudaStream_t str
     }
     const int64_t q_tiles = ((int64_t)p.max_query_len + 2 * kRows - 1) / (2 * kRows);
     if (q_tiles * p.num_heads > 0x7fffffff) return cudaErrorInvalidValue;
-    expanded_kernel<DN, DV><<<dim3((unsigned)(q_tiles * p.num_heads), p.batch), kThreads, Sh::kSmemBytes, stream>>>(
-        p, kv, (int)q_tiles, mq, mk, mv, mr);
-    return cudaGetLastError();
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(q_tiles * p.num_heads), p.batch);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = Sh::kSmemBytes;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;  // set up while the expansion ends
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = behind_expand ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, expanded_kernel<DN, DV>, p, kv, (int)q_tiles, mq, mk, mv, mr);
 }
 
 int64_t token_cap(int max_context_len) { return ((int64_t)max_context_len + 127) / 128 * 128; }
@@ -466,7 +478,8 @@ cudaError_t launch_latent_expanded(const LatentParams &p, const LatentWeights &w
         const cudaError_t e = launch_latent_expand(p, w, kv, sm_count, stream, fn);
         if (e != cudaSuccess) return e;
     }
-    return w.nope == 128 ? launch<128, 128>(p, kv, stream, fn) : launch<64, 64>(p, kv, stream, fn);
+    const bool behind = p.max_context_len > 0;
+    return w.nope == 128 ? launch<128, 128>(p, kv, behind, stream, fn) : launch<64, 64>(p, kv, behind, stream, fn);
 }
 
 }  // namespace kf

@@ -304,7 +304,6 @@ latent_kernel(const LatentParams p, const Partials part, const __grid_constant__
         mbar_init(o_empty, kSoftThreads);
         mbar_init(fin, 1);
         mbar_init(fin + 8, 1);
-        abort_flag = (*(volatile unsigned int *)p.err & KF_DEVERR_TIMEOUT) ? 1 : 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     if (warp == kProducerWarp && lane == 0) {
@@ -312,6 +311,9 @@ latent_kernel(const LatentParams p, const Partials part, const __grid_constant__
         asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tmap_q)) : "memory");
     }
     if (warp == kScoreWarp) tc05::tmem_alloc(smem_u32(&tmem_slot), 512);
+    // what ran before on the stream (an append, say) is complete from here on
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    if (threadIdx.x == 0) abort_flag = (*(volatile unsigned int *)p.err & KF_DEVERR_TIMEOUT) ? 1 : 0;
     Walker walk;
     int64_t slot0;
     const int64_t total = locate(
@@ -789,17 +791,21 @@ cudaError_t launch(const LatentParams &p, const Partials &part, int ctas, bool l
         if (e != cudaSuccess) return e;
         done.fetch_or(bit);
     }
-    latent_kernel<R><<<ctas, kThreads, Sh::kSmemBytes, stream>>>(p, part, mx, mq);
-    e = cudaGetLastError();
-    if (e != cudaSuccess || ctas == 1) return e;
     cudaLaunchConfig_t cfg = {};
-    cfg.blockDim = dim3(256);
+    cfg.gridDim = dim3(ctas);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = Sh::kSmemBytes;
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;  // set up while the attention kernel ends
+    // both kernels are set up while their predecessor ends, and wait for it themselves
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
+    e = cudaLaunchKernelEx(&cfg, latent_kernel<R>, p, part, mx, mq);
+    if (e != cudaSuccess || ctas == 1) return e;
+    cfg.blockDim = dim3(256);
+    cfg.dynamicSmemBytes = 0;
     if (long_units) {
         cfg.gridDim = dim3(ctas - 1, part.pitch);
         return cudaLaunchKernelEx(&cfg, latent_merge_kernel<R, 1>, p, part);

@@ -463,24 +463,31 @@ def _shape(t: torch.Tensor, shape, name: str) -> None:
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
-def _call(name: str, tensors, stream, *args) -> None:
-    """Call the library's `name` with the tensors' device current (they must share
-    one) and the stream appended to the arguments."""
-    index = tensors[0].get_device()
+def _call(name: str, index: int, stream, *args) -> None:
+    """Call the library's `name` with device `index` current and the stream
+    appended to the arguments."""
     if index < 0:
         raise ValueError("all tensors must be CUDA tensors")
-    for t in tensors:
-        if t is not None and t.get_device() != index:
-            raise ValueError("all tensors must be on cuda:%d, got one on %s" % (index, t.device))
     if index != torch.cuda.current_device():
         with torch.cuda.device(index):
-            return _call(name, tensors, stream, *args)
+            return _call(name, index, stream, *args)
     handle = _raw_stream(index) if stream is None and _raw_stream is not None else _stream(stream)
-    _check(getattr(_lib, name)(*args, handle), name)
+    status = getattr(_lib, name)(*args, handle)
+    if status != KF_OK:
+        raise KfError(status, name)
 
 
-def _opt(t: Optional[torch.Tensor], dtype, name: str) -> Optional[int]:
-    return None if t is None else _dev(t, dtype, name)
+def _on(index: int, t: torch.Tensor, dtype, name: str) -> int:
+    """The address of a contiguous tensor of `dtype` on device `index`."""
+    if t.dtype != dtype or t.get_device() != index or not t.is_contiguous():
+        if t.get_device() != index:
+            raise ValueError("%s must be on the call's device, cuda:%d, got %s" % (name, index, t.device))
+        return _dev(t, dtype, name)   # names what is wrong
+    return t.data_ptr()
+
+
+def _opt(index: int, t: Optional[torch.Tensor], dtype, name: str) -> Optional[int]:
+    return None if t is None else _on(index, t, dtype, name)
 
 
 KF_ROPE_DIM = 64  # width of the rotary part of a latent row
@@ -499,10 +506,11 @@ def kf_append_latent(latent_new: torch.Tensor, latent_cache: torch.Tensor, block
         _shape(row_start, (B + 1,), "row_start")
     elif n != B:
         raise ValueError("latent_new must hold one row a request without row_start")
-    _call("kf_append_latent", (latent_cache, latent_new, block_tables, context_lens_before, row_start), stream,
-          _dev(latent_new, torch.bfloat16, "latent_new"), _opt(row_start, torch.int32, "row_start"),
-          _dev(latent_cache, torch.bfloat16, "latent_cache"), _dev(block_tables, torch.int32, "block_tables"),
-          block_tables.shape[1], _dev(context_lens_before, torch.int32, "context_lens_before"), B, n, r, rope, bs, nb)
+    dev = latent_cache.get_device()
+    _call("kf_append_latent", dev, stream,
+          _on(dev, latent_new, torch.bfloat16, "latent_new"), _opt(dev, row_start, torch.int32, "row_start"),
+          _on(dev, latent_cache, torch.bfloat16, "latent_cache"), _on(dev, block_tables, torch.int32, "block_tables"),
+          block_tables.shape[1], _on(dev, context_lens_before, torch.int32, "context_lens_before"), B, n, r, rope, bs, nb)
 
 
 def kf_latent_workspace_size(batch: int, max_query_len: int, num_heads: int, latent_dim: int) -> int:
@@ -551,16 +559,17 @@ def kf_latent_attention(q: torch.Tensor, latent_cache: torch.Tensor, block_table
                         stream=None) -> Tuple[torch.Tensor, Optional[torch.Tensor]]:
     """Latent attention, absorbed form: q [Nq, H, R + 64] over the latent cache;
     returns (out [Nq, H, R], lse [Nq, H])."""
+    dev = q.get_device()
     nb, bs, r, rope = _latent_dims(latent_cache)
     out, code, lse_out = _latent_call(q, r + rope, r, block_tables, context_lens, q_start, out, out_dtype, lse_out,
                                       want_lse)
-    _call("kf_latent_attention", (q, latent_cache, block_tables, context_lens, workspace, q_start, out, lse_out), stream,
-          _dev(q, torch.bfloat16, "q"), _opt(q_start, torch.int32, "q_start"),
-          _dev(latent_cache, torch.bfloat16, "latent_cache"), _dev(block_tables, torch.int32, "block_tables"),
-          block_tables.shape[1], _dev(context_lens, torch.int32, "context_lens"), int(bool(causal)),
+    _call("kf_latent_attention", dev, stream,
+          _on(dev, q, torch.bfloat16, "q"), _opt(dev, q_start, torch.int32, "q_start"),
+          _on(dev, latent_cache, torch.bfloat16, "latent_cache"), _on(dev, block_tables, torch.int32, "block_tables"),
+          block_tables.shape[1], _on(dev, context_lens, torch.int32, "context_lens"), int(bool(causal)),
           int(max_context_len), int(max_query_len), block_tables.shape[0], q.shape[0], q.shape[1], r, rope, bs, nb,
-          float(scale), _dev(workspace, torch.uint8, "workspace"), workspace.numel(), _dev(out, out.dtype, "out"),
-          code, _opt(lse_out, torch.float32, "lse_out"))
+          float(scale), _on(dev, workspace, torch.uint8, "workspace"), workspace.numel(), _on(dev, out, out.dtype, "out"),
+          code, _opt(dev, lse_out, torch.float32, "lse_out"))
     return out, lse_out
 
 
@@ -586,6 +595,7 @@ def kf_latent_attention_expanded(q: torch.Tensor, latent_cache: torch.Tensor, w_
                                  want_lse: bool = True, stream=None) -> Tuple[torch.Tensor, Optional[torch.Tensor]]:
     """Latent attention, expanded form: q [Nq, H, Dn + 64], w_uk [H, Dn, R], w_uv
     [H, Dv, R]; returns (out [Nq, H, Dv], lse [Nq, H])."""
+    dev = q.get_device()
     nb, bs, r, rope = _latent_dims(latent_cache)
     if w_uk.dim() != 3 or w_uv.dim() != 3:
         raise ValueError("w_uk and w_uv must be [num_heads, width, latent_dim]")
@@ -594,20 +604,20 @@ def kf_latent_attention_expanded(q: torch.Tensor, latent_cache: torch.Tensor, w_
                                       want_lse)
     _shape(w_uk, (q.shape[1], dn, r), "w_uk")
     _shape(w_uv, (q.shape[1], dv, r), "w_uv")
-    _call("kf_latent_attention_expanded",
-          (q, latent_cache, w_uk, w_uv, block_tables, context_lens, workspace, q_start, out, lse_out), stream,
-          _dev(q, torch.bfloat16, "q"), _opt(q_start, torch.int32, "q_start"),
-          _dev(latent_cache, torch.bfloat16, "latent_cache"), _dev(w_uk, torch.bfloat16, "w_uk"),
-          _dev(w_uv, torch.bfloat16, "w_uv"), _dev(block_tables, torch.int32, "block_tables"),
-          block_tables.shape[1], _dev(context_lens, torch.int32, "context_lens"), int(bool(causal)),
+    _call("kf_latent_attention_expanded", dev, stream,
+          _on(dev, q, torch.bfloat16, "q"), _opt(dev, q_start, torch.int32, "q_start"),
+          _on(dev, latent_cache, torch.bfloat16, "latent_cache"), _on(dev, w_uk, torch.bfloat16, "w_uk"),
+          _on(dev, w_uv, torch.bfloat16, "w_uv"), _on(dev, block_tables, torch.int32, "block_tables"),
+          block_tables.shape[1], _on(dev, context_lens, torch.int32, "context_lens"), int(bool(causal)),
           int(max_context_len), int(max_query_len), block_tables.shape[0], q.shape[0], q.shape[1], r, rope, dn, dv,
-          bs, nb, float(scale), _dev(workspace, torch.uint8, "workspace"), workspace.numel(),
-          _dev(out, out.dtype, "out"), code, _opt(lse_out, torch.float32, "lse_out"))
+          bs, nb, float(scale), _on(dev, workspace, torch.uint8, "workspace"), workspace.numel(),
+          _on(dev, out, out.dtype, "out"), code, _opt(dev, lse_out, torch.float32, "lse_out"))
     return out, lse_out
 
 
 def _accumulate(name, q, k_cache, k_scale, block_tables, context_lens, max_context_len, scale, lse, scores_out,
                 scores_in, q_start, max_query_len, causal, stream):
+    dev = q.get_device()
     nq, hq, d = q.shape
     nb, bs, hkv, _ = k_cache.shape
     _shape(k_cache, (nb, bs, hkv, d), "k_cache")
@@ -624,14 +634,16 @@ def _accumulate(name, q, k_cache, k_scale, block_tables, context_lens, max_conte
         raise ValueError("q must hold one query token a request without q_start")
     if k_scale is not None:
         _shape(k_scale, (hkv,), "k_scale")
-    cache = _dev(k_cache, torch.bfloat16, "k_cache") if k_scale is None else _dev8(k_cache, "k_cache")
-    scales = () if k_scale is None else (_dev(k_scale, torch.float32, "k_scale"),)
-    _call(name, (q, k_cache, k_scale, block_tables, context_lens, lse, scores_out, scores_in, q_start), stream,
-          _dev(q, torch.bfloat16, "q"), _opt(q_start, torch.int32, "q_start"), cache, *scales,
-          _dev(block_tables, torch.int32, "block_tables"), block_tables.shape[1],
-          _dev(context_lens, torch.int32, "context_lens"), int(bool(causal)), int(max_context_len),
-          int(max_query_len), B, nq, hq, hkv, d, bs, nb, float(scale), _dev(lse, torch.float32, "lse"),
-          _opt(scores_in, torch.float32, "scores_in"), _dev(scores_out, torch.float32, "scores_out"),
+    if k_scale is not None and k_cache.get_device() != dev:
+        raise ValueError("k_cache must be on the call's device, cuda:%d, got %s" % (dev, k_cache.device))
+    cache = _on(dev, k_cache, torch.bfloat16, "k_cache") if k_scale is None else _dev8(k_cache, "k_cache")
+    scales = () if k_scale is None else (_on(dev, k_scale, torch.float32, "k_scale"),)
+    _call(name, dev, stream,
+          _on(dev, q, torch.bfloat16, "q"), _opt(dev, q_start, torch.int32, "q_start"), cache, *scales,
+          _on(dev, block_tables, torch.int32, "block_tables"), block_tables.shape[1],
+          _on(dev, context_lens, torch.int32, "context_lens"), int(bool(causal)), int(max_context_len),
+          int(max_query_len), B, nq, hq, hkv, d, bs, nb, float(scale), _on(dev, lse, torch.float32, "lse"),
+          _opt(dev, scores_in, torch.float32, "scores_in"), _on(dev, scores_out, torch.float32, "scores_out"),
           scores_out.shape[1])
     return scores_out
 
@@ -681,6 +693,7 @@ def kf_evict_tokens(caches, block_tables: torch.Tensor, context_lens: torch.Tens
     for c in caches:
         if c.dim() < 3 or c.shape != first.shape or c.dtype != first.dtype:
             raise ValueError("caches must share one [num_blocks, block_size, ...] shape and type")
+    dev = first.get_device()
     nb, bs = first.shape[:2]
     row_bytes = first.stride(1) * first.element_size()
     B = block_tables.shape[0]
@@ -692,15 +705,14 @@ def kf_evict_tokens(caches, block_tables: torch.Tensor, context_lens: torch.Tens
     for t, n in ((scores_out, "scores_out"), (positions, "positions"), (positions_out, "positions_out")):
         if t is not None:
             _shape(t, scores.shape, n)
-    ptr = [_dev(c, c.dtype, "caches") for c in caches] + [None]
-    _call("kf_evict_tokens", (*caches, block_tables, context_lens, scores, context_lens_out, scores_out, workspace,
-                              positions, seq_lens, positions_out), stream,
-          ptr[0], ptr[1], row_bytes, _dev(block_tables, torch.int32, "block_tables"), block_tables.shape[1],
-          _dev(context_lens, torch.int32, "context_lens"), int(max_context_len), B, bs, nb,
-          _dev(scores, torch.float32, "scores"), _dev(scores_out, torch.float32, "scores_out"), scores.shape[1],
-          _opt(positions, torch.int32, "positions"), _opt(positions_out, torch.int32, "positions_out"),
-          _opt(seq_lens, torch.int32, "seq_lens"), int(keep), int(sink), int(recent),
-          _dev(context_lens_out, torch.int32, "context_lens_out"), _dev(workspace, torch.uint8, "workspace"),
+    ptr = [_on(dev, c, c.dtype, "caches") for c in caches] + [None]
+    _call("kf_evict_tokens", dev, stream,
+          ptr[0], ptr[1], row_bytes, _on(dev, block_tables, torch.int32, "block_tables"), block_tables.shape[1],
+          _on(dev, context_lens, torch.int32, "context_lens"), int(max_context_len), B, bs, nb,
+          _on(dev, scores, torch.float32, "scores"), _on(dev, scores_out, torch.float32, "scores_out"), scores.shape[1],
+          _opt(dev, positions, torch.int32, "positions"), _opt(dev, positions_out, torch.int32, "positions_out"),
+          _opt(dev, seq_lens, torch.int32, "seq_lens"), int(keep), int(sink), int(recent),
+          _on(dev, context_lens_out, torch.int32, "context_lens_out"), _on(dev, workspace, torch.uint8, "workspace"),
           workspace.numel())
 
 
