@@ -7,7 +7,7 @@
 // so one tile of X in shared memory serves both products: keys as they are, values
 // as the same bytes read along the other axis.
 //
-// Work. Rows come in tiles of 64, tokens in tiles of 64. A unit is one row tile of
+// Work. Rows come in tiles of 64 (R = 512) or 128 (R = 256), tokens in tiles of 64. A unit is one row tile of
 // one request over all its token tiles; the units of the batch, laid end to end,
 // are cut into equal runs, one a CTA (one CTA an SM: the tile ring fills its
 // shared memory). A run may start and end inside a unit; the parts of such a unit
@@ -17,15 +17,15 @@
 //
 // One tile: 64 x (R + 64) bf16 arrive as four TMA boxes of 16 tokens, landing as
 // 8-token groups of 128-byte-swizzled atoms (group, 64-column atom, token, column).
-//   S[64 rows x 64 tokens]     = Q X^T          A = Q, B = X, both K-major, M = 64
+//   S[rows x 64 tokens]        = Q X^T          A = Q, B = X, both K-major, M = the row tile
 //   O^T[128 columns x rows]   += C^T P^T        A = C^T (M-major: the same tile), B = P
 // The value product is taken transposed, R / 128 instructions of M = 128 and N = the
-// rows in use (rounded up to 16): its accumulator then takes R / 128 * 64 TMEM
-// columns instead of R, which leaves room for two score tiles, and its work
+// rows in use (rounded up to 16): its accumulator then takes 256 TMEM columns instead
+// of R in every row's lane, which leaves room for two score tiles, and its work
 // shrinks with the rows. P goes through shared memory as that product's B.
-//   warps 0-3  softmax: rows 16 w .. 16 w + 15, four lanes a row (16x256b TMEM loads:
-//              lane l holds columns 8 i + 2 (l % 4), + 1 of rows l / 4 and l / 4 + 8);
-//              base-2 online softmax with a lazy maximum (it moves only by more
+//   warps 0-3  softmax; 64-row tiles: rows 16 w .. 16 w + 15, four lanes a row (16x256b
+//              TMEM loads: lane l holds columns 8 i + 2 (l % 4), + 1 of rows l / 4 and
+//              l / 4 + 8); 128-row tiles: a thread a row. Base-2 online softmax with a lazy maximum (it moves only by more
 //              than 8, and then O^T's columns are rescaled in TMEM); the epilogue.
 //   warp 4     TMA producer;  warp 5  issues S and owns TMEM;  warp 6  issues O^T.
 // Score tiles alternate between two TMEM buffers, and the two products have an issuing
@@ -54,25 +54,27 @@ namespace {
 using namespace tc;
 using namespace mq5;
 
-constexpr int kM = 64;   // rows a unit
+// Rows a unit: O^T takes R / 128 * (rows a unit) of TMEM's columns, 256 either way.
+__host__ __device__ constexpr int unit_rows(int latent_dim) { return latent_dim == 512 ? 64 : 128; }
 constexpr int kN = 64;   // tokens a tile
 constexpr int kAhead = 2;  // tiles fetched into L2 ahead of the ring's loads
 constexpr int kSoftThreads = 128, kProducerWarp = 4, kScoreWarp = 5, kValueWarp = 6, kThreads = 224;
 
 template <int R>
 struct LShape {
+    static constexpr int kM = unit_rows(R);
     static constexpr int kAtoms = (R + kRopeDim) / 64;
     static constexpr int kGroupBytes = kAtoms * 1024;         // 8 tokens
     static constexpr int kTileBytes = kN / 8 * kGroupBytes;
-    static constexpr int kQAtomBytes = kM * 128;              // 64 rows x 64 columns
+    static constexpr int kQAtomBytes = kM * 128;              // the rows x 64 columns
     static constexpr int kQBytes = kAtoms * kQAtomBytes;
     static constexpr int kPBytes = kM * kN * 2;
-    static constexpr int kStages = R == 512 ? 2 : 4;
+    static constexpr int kStages = R == 512 ? 2 : 3;
     static constexpr int kSmemBytes = kQBytes + kStages * kTileBytes + kPBytes + 1024;
     static constexpr int kDimTiles = R / 128;
     static constexpr uint32_t kColS = 256;                    // two score tiles; O^T below
     static_assert(kSmemBytes > 116 * 1024 && kSmemBytes <= 225 * 1024, "one CTA an SM");
-    static_assert(kDimTiles * 64 <= 256, "O^T columns");
+    static_assert(kDimTiles * kM <= 256, "O^T columns");
 };
 
 // ---------------------------------------------------------------------------
@@ -94,7 +96,8 @@ __device__ __forceinline__ Request request_of(const LatentParams &p, int b, bool
     q.L = r.L < p.max_context_len ? r.L : p.max_context_len;
     q.shift = r.L - r.C;
     q.n = q.L > 0 ? (q.L + kN - 1) / kN : 1;
-    q.units = (int)((q.rows + kM - 1) / kM);
+    const int M = unit_rows(p.latent_dim);
+    q.units = (int)((q.rows + M - 1) / M);
     return q;
 }
 
@@ -137,8 +140,9 @@ struct Walker {
             const int64_t unit = at.off / r.n, tile = at.off - unit * r.n;
             const int64_t len = left < r.n - tile ? left : r.n - tile;
             s.q0 = r.q0;
-            s.row0 = unit * kM;
-            s.rows = (int)(r.rows - s.row0 < kM ? r.rows - s.row0 : kM);
+            const int M = unit_rows(p.latent_dim);
+            s.row0 = unit * M;
+            s.rows = (int)(r.rows - s.row0 < M ? r.rows - s.row0 : M);
             s.L = r.L;
             s.shift = r.shift;
             s.b = at.b;
@@ -244,7 +248,7 @@ __device__ __forceinline__ void store_rows(uint32_t tm, bool any, int rows, cons
 #pragma unroll 1
         for (int r0 = 0; r0 < rows; r0 += 16) {
             uint32_t o[16];
-            if (any) tmem_ld16(tm + 64 * d + r0, o);
+            if (any) tmem_ld16(tm + unit_rows(R) * d + r0, o);
             float v[16];
 #pragma unroll
             for (int e = 0; e < 16; ++e) {
@@ -272,7 +276,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 latent_kernel(const LatentParams p, const Partials part, const __grid_constant__ CUtensorMap tmap_x,
               const __grid_constant__ CUtensorMap tmap_q) {
     using Sh = LShape<R>;
-    constexpr int NS = Sh::kStages, KS = (R + kRopeDim) / 16, KP = kN / 16;
+    constexpr int NS = Sh::kStages, KS = (R + kRopeDim) / 16, KP = kN / 16, kM = Sh::kM;
     // full[NS], empty[NS], q_full, q_empty, s_full[2], s_empty[2], p_full, pv_done, o_empty, fin[2]
     __shared__ __align__(8) uint64_t bar_mem[2 * NS + 11];
     __shared__ int64_t sm_loc[36];
@@ -467,7 +471,7 @@ latent_kernel(const LatentParams p, const Partials part, const __grid_constant__
                     for (int d = 0; d < Sh::kDimTiles; ++d)
 #pragma unroll
                         for (int kk = 0; kk < KP; ++kk)
-                            tc05::mma_ss(tm + 64 * d, cd + (uint64_t)((d * 2048 + kk * 2 * Sh::kGroupBytes) / 16),
+                            tc05::mma_ss(tm + kM * d, cd + (uint64_t)((d * 2048 + kk * 2 * Sh::kGroupBytes) / 16),
                                          pd + (uint64_t)(32 * kk / 16), id_o, (i > 0 || kk > 0) ? 1u : 0u);
                     tc05::commit(empty(st));
                     tc05::commit(pv_done);
@@ -481,15 +485,22 @@ latent_kernel(const LatentParams p, const Partials part, const __grid_constant__
         // ------------------------------- softmax --------------------------------
         const uint32_t lane_base = (uint32_t)(32 * warp) << 16;
         const float c = p.scale_log2;
-        const int rr[2] = {16 * warp + (lane >> 2), 16 * warp + (lane >> 2) + 8};  // this lane's rows
+        // This lane's rows and how their scores lie: 64 rows a unit, two rows, a quarter of
+        // each; 128 rows, one whole row.
+        constexpr int NR = kM == 64 ? 2 : 1, NX = 64 / (kM == 64 ? 4 : 1);
+        const int rr[2] = {kM == 64 ? 16 * warp + (lane >> 2) : (int)threadIdx.x, 16 * warp + (lane >> 2) + 8};
+        auto token_of = [&](int e) { return kM == 64 ? 8 * (e >> 1) + 2 * (lane & 3) + (e & 1) : e; };
         uint32_t g = 0;
         bool fail = false, stop = false;  // fail: this warp's wait gave up; stop: all four warps leave
         Cut cut{};
         Segment s{};
         while (!stop && walk.next(p, s)) {
-            float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
-            int lim[2];  // tokens these rows see (none: rows past the unit's last)
-            for (int k = 0; k < 2; ++k) {
+            float m[NR], l[NR];
+            int lim[NR];  // tokens these rows see (none: rows past the unit's last)
+#pragma unroll
+            for (int k = 0; k < NR; ++k) {
+                m[k] = -INFINITY;
+                l[k] = 0.f;
                 int64_t x = s.t_end;
                 if (p.causal && s.shift + (s.row0 + rr[k]) / p.num_heads + 1 < x)
                     x = s.shift + (s.row0 + rr[k]) / p.num_heads + 1;
@@ -500,8 +511,19 @@ latent_kernel(const LatentParams p, const Partials part, const __grid_constant__
                 const uint32_t sb = g & 1;
                 if (!warp_wait(s_full(sb), (g >> 1) & 1)) fail = true;
                 tc05::fence_after_sync();
-                uint32_t x[32];
-                tmem_ld_16x256b_x8(tm + lane_base + Sh::kColS + 64 * sb, x);
+                float x[NR][NX];  // element e of row k: token token_of(e) of the tile
+                if (kM == 64) {
+                    uint32_t u[32];
+                    tmem_ld_16x256b_x8(tm + lane_base + Sh::kColS + 64 * sb, u);
+#pragma unroll
+                    for (int e = 0; e < 32; ++e)  // (NR - 1 and NX - 1 are 1 and 15 here)
+                        x[(e >> 1) & (NR - 1)][(((e >> 2) << 1) | (e & 1)) & (NX - 1)] = __uint_as_float(u[e]);
+                } else {
+                    uint32_t u[64];
+                    tc05::tmem_ld64(tm + lane_base + Sh::kColS + 64 * sb, u);
+#pragma unroll
+                    for (int e = 0; e < 64; ++e) x[0][e & (NX - 1)] = __uint_as_float(u[e]);
+                }
                 tc05::fence_before_sync();
                 mbar_arrive(s_empty(sb));
                 // tokens past the last visible one: their rows become zeros
@@ -518,37 +540,40 @@ latent_kernel(const LatentParams p, const Partials part, const __grid_constant__
                                      : "memory");
                     }
                 }
-                float mx[2] = {-INFINITY, -INFINITY};
-                // fast path: both rows see the whole tile (so does the quad: lim goes by row)
-                // and the scale is positive; otherwise scores are scaled and masked first
-                const bool fast = c > 0.f && __all_sync(0xffffffffu, t0 + kN <= lim[0] && t0 + kN <= lim[1]);
+                float mx[NR];
+                // fast path: all rows of the warp see the whole tile and the scale is positive;
+                // otherwise scores are scaled and masked first
+                bool whole_tile = true;
+#pragma unroll
+                for (int k = 0; k < NR; ++k) {
+                    mx[k] = -INFINITY;
+                    whole_tile = whole_tile && t0 + kN <= lim[k];
+                }
+                const bool fast = c > 0.f && __all_sync(0xffffffffu, whole_tile);
                 if (fast) {
 #pragma unroll
-                    for (int e = 0; e < 8; ++e)
+                    for (int k = 0; k < NR; ++k) {
 #pragma unroll
-                        for (int k = 0; k < 2; ++k)
-                            mx[k] = max3f(mx[k], __uint_as_float(x[4 * e + 2 * k]), __uint_as_float(x[4 * e + 2 * k + 1]));
-                    mx[0] *= c;
-                    mx[1] *= c;
+                        for (int e = 0; e < NX; e += 2) mx[k] = max3f(mx[k], x[k][e], x[k][e + 1]);
+                        mx[k] *= c;
+                    }
                 } else {
 #pragma unroll
-                    for (int e = 0; e < 8; ++e)
+                    for (int k = 0; k < NR; ++k)
 #pragma unroll
-                        for (int k = 0; k < 2; ++k)
-#pragma unroll
-                            for (int u = 0; u < 2; ++u) {
-                                const int t = t0 + 8 * e + 2 * (lane & 3) + u;
-                                const float v = t < lim[k] ? __uint_as_float(x[4 * e + 2 * k + u]) * c : -INFINITY;
-                                x[4 * e + 2 * k + u] = __float_as_uint(v);
-                                mx[k] = fmaxf(mx[k], v);
-                            }
+                        for (int e = 0; e < NX; ++e) {
+                            x[k][e] = t0 + token_of(e) < lim[k] ? x[k][e] * c : -INFINITY;
+                            mx[k] = fmaxf(mx[k], x[k][e]);
+                        }
                 }
                 bool need = false;
-                float alpha[2];
+                float alpha[NR];
 #pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                    mx[k] = fmaxf(mx[k], __shfl_xor_sync(0xffffffffu, mx[k], 1));
-                    mx[k] = fmaxf(mx[k], __shfl_xor_sync(0xffffffffu, mx[k], 2));
+                for (int k = 0; k < NR; ++k) {
+                    if (kM == 64) {
+                        mx[k] = fmaxf(mx[k], __shfl_xor_sync(0xffffffffu, mx[k], 1));
+                        mx[k] = fmaxf(mx[k], __shfl_xor_sync(0xffffffffu, mx[k], 2));
+                    }
                     const bool up = mx[k] > m[k] + kRescaleSlack;
                     alpha[k] = up ? exp2f(m[k] - mx[k]) : 1.f;  // m = -inf: 0
                     if (up) {
@@ -566,53 +591,66 @@ latent_kernel(const LatentParams p, const Partials part, const __grid_constant__
                 if (any) {
                     stop = soft_any(fail);
                     if (stop) break;
-                    if ((lane & 3) == 0) {
-                        sm_alpha[rr[0]] = alpha[0];
-                        sm_alpha[rr[1]] = alpha[1];
-                    }
+#pragma unroll
+                    for (int k = 0; k < NR; ++k)
+                        if (kM == 128 || (lane & 3) == 0) sm_alpha[rr[k]] = alpha[k];
                     soft_sync();
                     tc05::fence_after_sync();
                     for (int d = 0; d < Sh::kDimTiles; ++d)
                         for (int q = 0; q < (s.rows + 15) / 16; ++q) {
                             uint32_t o[16];
-                            tmem_ld16(tm + lane_base + 64 * d + 16 * q, o);
+                            tmem_ld16(tm + lane_base + kM * d + 16 * q, o);
 #pragma unroll
                             for (int e = 0; e < 16; ++e)
                                 o[e] = __float_as_uint(__uint_as_float(o[e]) * sm_alpha[16 * q + e]);
-                            tc05::tmem_st16(tm + lane_base + 64 * d + 16 * q, o);
+                            tc05::tmem_st16(tm + lane_base + kM * d + 16 * q, o);
                         }
                 }
 #pragma unroll
-                for (int k = 0; k < 2; ++k) {
+                for (int k = 0; k < NR; ++k) {
                     const float mu = m[k] == -INFINITY ? 0.f : m[k];
                     const float cc = fast ? c : 1.f;  // (scores are scaled already on the slow path)
                     const uint32_t row = sP + rr[k] * 128;
                     float2 ls = make_float2(0.f, 0.f);
+                    uint32_t w[NX / 2];
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        float2 a = fma_f32x2(
-                            make_float2(__uint_as_float(x[4 * e + 2 * k]), __uint_as_float(x[4 * e + 2 * k + 1])),
-                            make_float2(cc, cc), make_float2(-mu, -mu));
+                    for (int e = 0; e < NX / 2; ++e) {
+                        float2 a = fma_f32x2(make_float2(x[k][2 * e], x[k][2 * e + 1]), make_float2(cc, cc),
+                                             make_float2(-mu, -mu));
                         a.x = ex2f(a.x);
                         a.y = ex2f(a.y);
                         ls = add_f32x2(ls, a);
-                        asm volatile("st.shared.u32 [%0], %1;" ::"r"(row + ((e ^ (rr[k] & 7)) << 4) + (lane & 3) * 4),
-                                     "r"(pack_bf16(a.x, a.y))
-                                     : "memory");
+                        w[e] = pack_bf16(a.x, a.y);
                     }
                     l[k] += ls.x + ls.y;
+                    if (kM == 64) {
+#pragma unroll
+                        for (int e = 0; e < NX / 2; ++e)
+                            asm volatile("st.shared.u32 [%0], %1;" ::"r"(row + ((e ^ (rr[k] & 7)) << 4) + (lane & 3) * 4),
+                                         "r"(w[e])
+                                         : "memory");
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 8; ++e)
+                            asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(row + ((e ^ (rr[k] & 7)) << 4)),
+                                         "r"(w[(4 * e) % (NX / 2)]), "r"(w[(4 * e + 1) % (NX / 2)]),
+                                         "r"(w[(4 * e + 2) % (NX / 2)]), "r"(w[(4 * e + 3) % (NX / 2)])
+                                         : "memory");
+                    }
                 }
                 fence_proxy_async_smem();
                 tc05::fence_before_sync();
                 mbar_arrive(p_full);
             }
             if (stop) break;
-            // epilogue: row sums over the four lanes of a row, then O^T column by column
+            // epilogue: row sums (over the lanes of a row), then O^T column by column
 #pragma unroll
-            for (int k = 0; k < 2; ++k) {
-                l[k] += __shfl_xor_sync(0xffffffffu, l[k], 1);
-                l[k] += __shfl_xor_sync(0xffffffffu, l[k], 2);
-                if ((lane & 3) == 0) {
+            for (int k = 0; k < NR; ++k) {
+                if (kM == 64) {
+                    l[k] += __shfl_xor_sync(0xffffffffu, l[k], 1);
+                    l[k] += __shfl_xor_sync(0xffffffffu, l[k], 2);
+                }
+                if (kM == 128 || (lane & 3) == 0) {
                     sm_alpha[rr[k]] = l[k] > 0.f ? 1.f / l[k] : 0.f;
                     sm_lse[rr[k]] = l[k] > 0.f ? (m[k] + log2f(l[k])) * 0.6931471805599453f : -INFINITY;
                 }
@@ -746,18 +784,18 @@ latent_merge_kernel(const LatentParams p, const Partials part) {
     if (lane == 0 && p.lse_out) p.lse_out[out_row] = W > 0.f ? M + logf(W) : -INFINITY;
 }
 
-int64_t row_pitch(int max_query_len, int num_heads) {
+int64_t row_pitch(int max_query_len, int num_heads, int latent_dim) {
     const int64_t rows = (int64_t)max_query_len * num_heads;
-    return rows < kM ? rows : kM;
+    return std::min<int64_t>(rows, unit_rows(latent_dim));
 }
 
-// (64 columns, rows, column atoms): a box of 64 rows x all columns lands as atoms of
-// 64 rows x 128 swizzled bytes.
+// (64 columns, rows, column atoms): a box of a unit's rows x all columns lands as atoms
+// of those rows x 128 swizzled bytes.
 bool encode_q(tc::EncodeFn fn, CUtensorMap *map, const LatentParams &p) {
     const int width = p.latent_dim + kRopeDim;
     const cuuint64_t dims[3] = {64, (cuuint64_t)p.num_q_tokens * p.num_heads, (cuuint64_t)width / 64};
     const cuuint64_t strides[2] = {(cuuint64_t)width * 2, 128};
-    const cuuint32_t box[3] = {64, (cuuint32_t)kM, (cuuint32_t)width / 64};
+    const cuuint32_t box[3] = {64, (cuuint32_t)unit_rows(p.latent_dim), (cuuint32_t)width / 64};
     const cuuint32_t estr[3] = {1, 1, 1};
     return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<uint16_t *>(p.q), dims, strides, box, estr,
               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
@@ -821,7 +859,7 @@ size_t al256(size_t x) { return (x + 255) & ~(size_t)255; }
 }  // namespace
 
 size_t latent_workspace_bytes(int batch, int max_query_len, int num_heads, int latent_dim, int sm_count) {
-    const size_t rows = 2 * (size_t)sm_count * row_pitch(max_query_len, num_heads);
+    const size_t rows = 2 * (size_t)sm_count * row_pitch(max_query_len, num_heads, latent_dim);
     return al256(rows * latent_dim * 4) + al256(rows * 4) + sm_count * sizeof(Cut);
 }
 
@@ -830,11 +868,12 @@ cudaError_t launch_latent(const LatentParams &p, void *workspace, int sm_count, 
     CUtensorMap mx, mq;
     if (!encode_cache(fn, &mx, p) || !encode_q(fn, &mq, p)) return cudaErrorInvalidValue;
     // no more CTAs than the batch can have tiles
-    const int64_t units = (int64_t)p.batch * (((int64_t)p.max_query_len * p.num_heads + kM - 1) / kM);
+    const int M = unit_rows(p.latent_dim);
+    const int64_t units = (int64_t)p.batch * (((int64_t)p.max_query_len * p.num_heads + M - 1) / M);
     const int64_t tiles = units * std::max<int64_t>(1, ((int64_t)p.max_context_len + kN - 1) / kN);
     const int ctas = (int)std::min<int64_t>(sm_count, tiles);
     Partials part;
-    part.pitch = (int)row_pitch(p.max_query_len, p.num_heads);
+    part.pitch = (int)row_pitch(p.max_query_len, p.num_heads, p.latent_dim);
     part.o = static_cast<float *>(workspace);
     const size_t rows = 2 * (size_t)sm_count * part.pitch;
     uint8_t *ws = static_cast<uint8_t *>(workspace) + al256(rows * p.latent_dim * 4);
