@@ -516,7 +516,9 @@ kf_status kf_append_latent(const void *latent_new, const int32_t *row_start, voi
  *
  * A row that sees no token (an empty request, or the first C_b - L_b queries of
  * a causal call with C_b > L_b) gives out = 0 and lse = -inf. Rows of q that no
- * request owns are left as they were in out and lse_out. Scores, softmax
+ * request owns are left as they were in out and lse_out. What the cache holds
+ * past context_lens may be anything; a NaN or infinity in a row that some query of
+ * a request sees can reach that request's other queries. Scores, softmax
  * statistics and sums are fp32; the softmax weights enter the value product as
  * bf16 (the cache's type), the sum that normalises them does not.
  * Host errors as kf_paged_multiquery_attention; a missing or short workspace ->

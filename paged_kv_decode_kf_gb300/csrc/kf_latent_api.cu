@@ -91,7 +91,10 @@ kf_status accumulate_impl(const void *q, const int32_t *q_start, const void *k_c
     if ((head_dim != 64 && head_dim != 128) || !block_ok(block_size) || num_q_heads % num_kv_heads != 0 ||
         (group != 1 && group != 2 && group != 4 && group != 8))
         return KF_ERR_UNSUPPORTED;
-    if (batch > 65535) return KF_ERR_UNSUPPORTED;
+    // q's rows and the cache's 8-token groups fit 31 bits (TMA coordinates, column counts)
+    if (batch > 65535 || (int64_t)num_q_tokens * num_q_heads > 0x7fffffff ||
+        num_blocks * (block_size / 8) > 0x7fffffff)
+        return KF_ERR_UNSUPPORTED;
     AccumulateParams p;
     int sms = 0;
     if (device_facts(&p.err, &sms) != cudaSuccess) return KF_ERR_CUDA;

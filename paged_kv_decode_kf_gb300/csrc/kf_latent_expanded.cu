@@ -371,7 +371,7 @@ expanded_kernel(const LatentParams p, const ExpandedKV kv, int q_tiles, const __
         }
         if (ok && warp_wait(fin, 0)) {
             tc05::fence_after_sync();
-            const float inv = l > 0.f ? 1.f / l : 0.f;
+            const float inv = l != 0.f ? 1.f / l : 0.f;  // (no token seen: 0; a NaN stays one)
 #pragma unroll
             for (int cc = 0; cc < DV / 32; ++cc) {
                 uint32_t o[32];
@@ -379,7 +379,7 @@ expanded_kernel(const LatentParams p, const ExpandedKV kv, int q_tiles, const __
                 if (!row_ok) continue;
                 float v[32];
 #pragma unroll
-                for (int i = 0; i < 32; ++i) v[i] = l > 0.f ? __uint_as_float(o[i]) * inv : 0.f;
+                for (int i = 0; i < 32; ++i) v[i] = l != 0.f ? __uint_as_float(o[i]) * inv : 0.f;
                 if (p.out_dtype == KF_F32) {
                     float4 *dst = reinterpret_cast<float4 *>(static_cast<float *>(p.out) + at * DV + 32 * cc);
 #pragma unroll
@@ -392,7 +392,7 @@ expanded_kernel(const LatentParams p, const ExpandedKV kv, int q_tiles, const __
                                             pack_bf16(v[8 * i + 4], v[8 * i + 5]), pack_bf16(v[8 * i + 6], v[8 * i + 7]));
                 }
             }
-            if (row_ok && p.lse_out) p.lse_out[at] = l > 0.f ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
+            if (row_ok && p.lse_out) p.lse_out[at] = l != 0.f ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
         } else {
             if (r == 0) raise_error(p.err, KF_DEVERR_TIMEOUT);
             abort_flag = 1;

@@ -253,7 +253,7 @@ __device__ __forceinline__ void store_rows(uint32_t tm, bool any, int rows, cons
 #pragma unroll
             for (int e = 0; e < 16; ++e) {
                 const float w = inv[r0 + e];
-                v[e] = any && w > 0.f ? __uint_as_float(o[e]) * w : 0.f;
+                v[e] = any && w != 0.f ? __uint_as_float(o[e]) * w : 0.f;
             }
             // (a branch a store costs three times the stores: only the last chunk pays it)
             if (r0 + 16 <= rows) {
@@ -651,8 +651,9 @@ latent_kernel(const LatentParams p, const Partials part, const __grid_constant__
                     l[k] += __shfl_xor_sync(0xffffffffu, l[k], 2);
                 }
                 if (kM == 128 || (lane & 3) == 0) {
-                    sm_alpha[rr[k]] = l[k] > 0.f ? 1.f / l[k] : 0.f;
-                    sm_lse[rr[k]] = l[k] > 0.f ? (m[k] + log2f(l[k])) * 0.6931471805599453f : -INFINITY;
+                    // (no token seen: 0 and -inf; a NaN stays one)
+                    sm_alpha[rr[k]] = l[k] != 0.f ? 1.f / l[k] : 0.f;
+                    sm_lse[rr[k]] = l[k] != 0.f ? (m[k] + log2f(l[k])) * 0.6931471805599453f : -INFINITY;
                 }
             }
             if (s.tiles > 0 && !warp_wait(pv_done, (g - 1) & 1)) fail = true;
@@ -730,8 +731,14 @@ latent_merge_kernel(const LatentParams p, const Partials part) {
 #pragma unroll
     for (int v = 0; v < V; ++v) acc[v] = make_float4(0.f, 0.f, 0.f, 0.f);
     if (live) {
-        for (int i = lane; i < n; i += 32) M = fmaxf(M, part.lse[slot_at(i) * part.pitch + row]);
+        bool nan = false;
+        for (int i = lane; i < n; i += 32) {
+            const float x = part.lse[slot_at(i) * part.pitch + row];
+            nan = nan || x != x;
+            M = fmaxf(M, x);
+        }
         for (int o = 16; o; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+        if (__any_sync(0xffffffffu, nan)) M = NAN;  // a NaN row's weights, and so the row, are NaN
         if (M != -INFINITY) {
 #pragma unroll 4
             for (int i = sub; i < n; i += WPR) {
@@ -771,7 +778,7 @@ latent_merge_kernel(const LatentParams p, const Partials part) {
     }
     if (!live) return;
     const int64_t out_row = cut.row_out + row;
-    const float inv = W > 0.f ? 1.f / W : 0.f;
+    const float inv = W != 0.f ? 1.f / W : 0.f;
 #pragma unroll
     for (int v = 0; v < V; ++v) {
         const float4 x = make_float4(acc[v].x * inv, acc[v].y * inv, acc[v].z * inv, acc[v].w * inv);
@@ -781,7 +788,7 @@ latent_merge_kernel(const LatentParams p, const Partials part) {
             *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(p.out) + e) =
                 make_uint2(pack_bf16(x.x, x.y), pack_bf16(x.z, x.w));
     }
-    if (lane == 0 && p.lse_out) p.lse_out[out_row] = W > 0.f ? M + logf(W) : -INFINITY;
+    if (lane == 0 && p.lse_out) p.lse_out[out_row] = W != 0.f ? M + logf(W) : -INFINITY;
 }
 
 int64_t row_pitch(int max_query_len, int num_heads, int latent_dim) {

@@ -95,6 +95,27 @@ def test_accumulate_windows(kf, fp8, causal, hq, hkv, D):
     _run_acc(kf, a, lens, counts, causal, alias=True)
 
 
+@pytest.mark.parametrize("fp8", [False, True])
+def test_accumulate_long_windows_and_few_tokens(kf, fp8):
+    """Several groups of 128 columns, more queries than tokens, many requests."""
+    lens, counts = [150, 3, 129, 20], [70, 9, 1, 20]
+    a = _acc_inputs(lens, counts, 16, 2, 128, 16, fp8, seed=91)
+    _run_acc(kf, a, lens, counts, True)
+    lens, counts = [(7 * i) % 40 for i in range(400)], [i % 3 for i in range(400)]
+    a = _acc_inputs(lens, counts, 8, 1, 64, 32, fp8, seed=92)
+    _run_acc(kf, a, lens, counts, True)
+    lens = [(11 * i) % 40 for i in range(400)]
+    a = _acc_inputs(lens, [1] * 400, 8, 1, 64, 32, fp8, seed=93)
+    _run_acc(kf, a, lens, [1] * 400, True)
+
+
+def test_accumulate_no_queries(kf):
+    """No query at all: the scores come through."""
+    lens, counts = [30, 5], [0, 0]
+    a = _acc_inputs(lens, counts, 8, 2, 128, 16, False, seed=94)
+    _run_acc(kf, a, lens, counts, True)
+
+
 def test_accumulate_rows_without_weight_and_masked_nan(kf):
     lens, counts = [50, 20], [3, 1]
     a = list(_acc_inputs(lens, counts, 8, 2, 128, 16, False, seed=77))
@@ -188,6 +209,46 @@ def test_evict_one_of_many(kf):
 
 def test_evict_long(kf):
     _evict_case(kf, [70001, 5], 9001, 4, 1000, 16, 1, False, 6)
+
+
+def test_evict_wide_and_few_moves(kf):
+    """A cluster a request that moves its rows itself, and keys beyond shared memory."""
+    _evict_case(kf, [9000, 8991, 8990, 100], 8990, 4, 100, 64, 2, True, 10)
+    _evict_case(kf, [400001], 399990, 0, 5, 16, 1, False, 11)
+    _evict_case(kf, [400001], 1000, 4, 5, 16, 1, False, 12)
+
+
+def test_evict_many_requests(kf):
+    _evict_case(kf, [20 + i % 50 for i in range(300)], 40, 2, 8, 32, 1, True, 13)
+
+
+def test_evict_graph(kf):
+    """A captured call follows new scores."""
+    g = torch.Generator().manual_seed(14)
+    cache, table = ref.paged([100, 60], 16, 8, g)
+    d, t = cache.cuda(), table.cuda()
+    ctx = torch.tensor([100, 60], dtype=torch.int32, device="cuda")
+    out_ctx = torch.zeros_like(ctx)
+    sc = torch.rand(2, 100, device="cuda")
+    so = torch.zeros_like(sc)
+    ws = kf.make_evict_workspace(2, 100, 30)
+
+    def step():
+        kf.kf_evict_tokens([d], t, ctx, 100, sc, 30, 1, 4, out_ctx, so, ws)
+    step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    for seed in (1, 2):
+        torch.manual_seed(seed)
+        d.copy_(cache)
+        sc.copy_(torch.rand(2, 100))
+        graph.replay()
+        torch.cuda.synchronize()
+        for b, (n, at) in enumerate(ref.evict([100, 60], sc.cpu(), 30, 1, 4)):
+            assert np.array_equal(ref.rows_of(d.cpu(), table, b, n), ref.rows_of(cache, table, b, int(ctx[b]))[at])
+            assert np.array_equal(so[b, :n].cpu().numpy(), sc[b].cpu().numpy()[at])
 
 
 def test_evict_special_scores(kf):

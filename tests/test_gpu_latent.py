@@ -255,6 +255,44 @@ def test_absorbed_graph(kf):
         c.check(out.cpu(), lse.cpu())
 
 
+@pytest.mark.parametrize("R", [512, 256])
+def test_absorbed_more_queries_than_tokens(kf, R):
+    """C > L, causal: the first C - L queries see nothing."""
+    c = Case([2, 70, 0], [5, 3, 2], 20, R, seed=33)
+    out, lse = c.run(kf)
+    c.check(out, lse)
+    assert np.all(np.isneginf(lse[:3].numpy())) and float(out[:3].abs().max()) == 0.0
+
+
+@pytest.mark.parametrize("R", [512, 256])
+def test_absorbed_many_small_requests(kf, R):
+    """More requests than threads search for the runs."""
+    lens = [(7 * i) % 50 for i in range(700)]
+    c = Case(lens, [1] * 700, 2, R, seed=35)
+    out, lse = c.run(kf)
+    c.check(out, lse)
+
+
+@pytest.mark.parametrize("lens", [[40, 50], [3000, 50]])
+def test_absorbed_nan_query_stays_its_own(kf, lens):
+    c = Case(lens, [1, 1], 16, 512, seed=37)
+    clean, clean_lse = c.run(kf)
+    c.q[0, 3, 5] = float("nan")
+    out, lse = c.run(kf)
+    assert torch.isnan(out[0, 3]).all() and torch.isnan(lse[0, 3])
+    keep = torch.ones(2, 16, dtype=torch.bool)
+    keep[0, 3] = False
+    assert torch.equal(out[keep], clean[keep]) and torch.equal(lse[keep], clean_lse[keep])
+
+
+def test_absorbed_negative_and_zero_scale(kf):
+    for scale in (-0.04, 0.0):
+        c = Case([90, 33], [2, 1], 16, 512, seed=39)
+        c.scale = scale
+        out, lse = c.run(kf)
+        c.check(out, lse)
+
+
 def test_absorbed_device_errors(kf):
     c = Case([40, 50, 60], [1, 1, 1], 16, 512, seed=31)
     good = c.run(kf)[0]
@@ -306,6 +344,63 @@ def test_expanded_masked_nan(kf):
     clean = Case([70, 33], [3, 33], 2, 512, 16, seed=47, w=128)
     out, lse = c.run(kf)
     clean.check(out, lse)
+
+
+def test_expanded_more_queries_than_tokens(kf):
+    c = Case([2, 70, 0], [140, 3, 2], 2, 256, 16, seed=53, w=64)
+    out, lse = c.run(kf)
+    c.check(out, lse)
+
+
+def test_expanded_many_small_requests(kf):
+    """More requests than the blocks sort, and a batch that they do."""
+    for n in (330, 40):
+        c = Case([1 + (5 * i) % 20 for i in range(n)], [1] * n, 1, 256, 16, seed=55, w=64)
+        out, lse = c.run(kf)
+        c.check(out, lse)
+
+
+def test_expanded_nan_query_and_scales(kf):
+    c = Case([60, 50], [30, 7], 2, 512, 16, seed=57, w=128)
+    clean, clean_lse = c.run(kf)
+    c.q[4, 1, 5] = float("nan")
+    out, lse = c.run(kf)
+    assert torch.isnan(out[4, 1]).all() and torch.isnan(lse[4, 1])
+    keep = torch.ones(37, 2, dtype=torch.bool)
+    keep[4, 1] = False
+    assert torch.equal(out[keep], clean[keep]) and torch.equal(lse[keep], clean_lse[keep])
+    for scale in (-0.05, 0.0):
+        c = Case([60, 50], [30, 7], 2, 512, 16, seed=57, w=128)
+        c.scale = scale
+        out, lse = c.run(kf)
+        c.check(out, lse)
+
+
+def test_expanded_graph(kf):
+    """A captured call follows new contents of its buffers."""
+    c = Case([100, 70], [40, 70], 2, 256, 16, seed=59, w=64)
+    q, cache, table, ctx, qs = c.dev()
+    wk, wv = c.w_uk.cuda(), c.w_uv.cuda()
+    ws = kf.make_latent_expanded_workspace(2, q.shape[0], 100, 2, 64, 64)
+    out = torch.zeros(q.shape[0], 2, 64, device="cuda")
+    lse = torch.zeros(q.shape[0], 2, device="cuda")
+
+    def step():
+        kf.kf_latent_attention_expanded(q, cache, wk, wv, table, ctx, 100, c.scale, ws, q_start=qs, max_query_len=70,
+                                        out=out, lse_out=lse)
+    step()
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        step()
+    for seed in (1, 2):
+        torch.manual_seed(seed)
+        cache.copy_(torch.randn(cache.shape).to(torch.bfloat16))
+        q.copy_(torch.randn(q.shape).to(torch.bfloat16))
+        g.replay()
+        torch.cuda.synchronize()
+        c.q, c.cache = q.cpu(), cache.cpu()
+        c.check(out.cpu(), lse.cpu())
 
 
 def test_expanded_agrees_with_absorbed(kf):

@@ -108,7 +108,8 @@ def test_accumulate_host_checks(kf, fp8):
                 dict(ss=63), dict(qs=None), dict(hq=0), dict(hkv=0), dict(d=0), dict(scale=float("inf")),
                 dict(causal=-1), dict(st=0), dict(nb=0)) + ((dict(ks=None),) if fp8 else ()):
         assert _acc(lib, fp8, **bad) == kf.KF_ERR_INVALID, bad
-    for bad in (dict(d=96), dict(bs=64), dict(hq=6), dict(hq=32, hkv=2), dict(hq=7, hkv=2), dict(B=70000)):
+    for bad in (dict(d=96), dict(bs=64), dict(hq=6), dict(hq=32, hkv=2), dict(hq=7, hkv=2), dict(B=70000),
+                dict(n=1 << 30), dict(nb=1 << 40)):
         assert _acc(lib, fp8, **bad) == kf.KF_ERR_UNSUPPORTED, bad
 
 
