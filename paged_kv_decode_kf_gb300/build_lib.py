@@ -28,7 +28,8 @@ HEADERS = [os.path.join(CSRC, "kf_internal.cuh"), os.path.join(CSRC, "kf_decode_
            os.path.join(CSRC, "kf_decode_bal.cuh"),
            os.path.join(CSRC, "kf_tc05.cuh"), os.path.join(CSRC, "kf_mq_tc05.cuh"),
            os.path.join(CSRC, "kf_latent.cuh"), os.path.join(CSRC, "kf_latent_expanded.cuh"),
-           os.path.join(CSRC, "kf_runs.cuh"), os.path.join(CSRC, "kf_evict.cuh"),
+           os.path.join(CSRC, "kf_runs.cuh"), os.path.join(CSRC, "kf_device.cuh"),
+           os.path.join(CSRC, "kf_tc05_ops.cuh"), os.path.join(CSRC, "kf_evict.cuh"),
            os.path.join(ROOT, "include", "kf.h")]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ARCH + ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-I" + os.path.join(ROOT, "include")]

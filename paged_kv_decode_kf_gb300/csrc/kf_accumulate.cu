@@ -14,8 +14,9 @@
 // as K and Q agree, so a lane's fragment is 16 consecutive bytes of a K row, loaded
 // from global memory straight into registers: no shared memory, no barrier, and the
 // four lanes of a row cover 64 contiguous bytes a load. A warp holds 32 tokens of
-// one head (64 registers at D = 128), sixteen warps an SM some 128 KB in flight,
-// against the 45-60 KB that cover HBM's latency. Q comes through L1.
+// one head (64 E4M3 ones; 64 registers at D = 128), twelve warps an SM some 96 KB in
+// flight, against the 45-60 KB that cover HBM's latency. Q comes through L1.
+// Measured: 64 requests of 4K tokens, 32 / 8 heads, bf16: 90 us, 5.7 TB/s of K.
 // E4M3 keys widen to fp16 (exact); q goes to fp16 times a power of two that puts
 // the row's largest magnitude just below 2^15 (exact for every number within 2^-29
 // of it), undone with the key's scale.
@@ -35,7 +36,15 @@ namespace {
 
 using namespace tc;
 
-constexpr int kWarps = 4, kTiles = 2;  // warps a CTA; 16-token tiles a warp holds
+constexpr int kWarps = 4;  // warps a CTA
+// 16-token tiles a warp holds, and CTAs an SM: as many keys in flight either way, and
+// enough of them a warp to pay for q's conversion (64 requests of 4K, bf16: 90 us with
+// 2 tiles x 3 CTAs, 93 with 2 x 4, 96 with 1 x 6 and 4 x 2; ragged E4M3: 145 us with
+// 4 x 3, 155 with 2 x 4, 199 with 1 x 6).
+template <bool KV8>
+struct Held {
+    static constexpr int kTiles = KV8 ? 4 : 2, kCtas = 3;
+};
 
 __device__ __forceinline__ uint4 load_stream(const void *p) {
     uint4 v;
@@ -237,8 +246,9 @@ __device__ __forceinline__ void key_rows(const AccumulateParams &p, int b, int64
 }
 
 template <int D, bool KV8>
-__global__ void __launch_bounds__(32 * kWarps, 4)
+__global__ void __launch_bounds__(32 * kWarps, Held<KV8>::kCtas)
 accumulate_kernel(const AccumulateParams p) {
+    constexpr int kTiles = Held<KV8>::kTiles;
     constexpr int NL = KV8 ? D / 64 : D / 32;   // 16-byte loads a lane and K row
     constexpr int EB = KV8 ? 1 : 2;
     __shared__ int64_t sm_loc[36];
@@ -418,7 +428,8 @@ cudaError_t launch(const AccumulateParams &p, int sm_count, cudaStream_t stream,
     const int64_t tiles = (int64_t)p.batch * ((p.max_context_len + 15) / 16);
     // one wave of resident CTAs, no more warps (CTAs) than the batch can have tiles (runs)
     if (cols <= 8) {
-        const int64_t ctas = (tiles + kWarps - 1) / kWarps < 4ll * sm_count ? (tiles + kWarps - 1) / kWarps : 4ll * sm_count;
+        const int64_t wave = (int64_t)Held<KV8>::kCtas * sm_count, need = (tiles + kWarps - 1) / kWarps;
+        const int64_t ctas = need < wave ? need : wave;
         accumulate_kernel<D, KV8><<<(unsigned)ctas, 32 * kWarps, 0, stream>>>(p);
     } else {
         const int64_t runs = (int64_t)p.batch * ((p.max_context_len + 16 * kWinTiles - 1) / (16 * kWinTiles));

@@ -9,9 +9,10 @@
 //
 // One CTA a run of 128-token tiles, each tile over all heads: per (head, 128 columns)
 // 32 KB of Q, per head 32 KB of K (D = 128), 512 cycles of products and 16384
-// exponentials, 1024 cycles of the SM's exponential unit: that unit is the bound. The
-// kernel it replaces for bf16 windows (mma.sync, keys in registers) took 66 us on 4
-// requests of 4K-12K tokens and 32 queries, bound by its fragment loads.
+// exponentials, 1024 cycles of the SM's exponential unit: that unit is the bound of
+// long runs. 4 requests of 4K-12K tokens, 32 queries of 32 / 8 heads: 25 us (a third of
+// it the start and the two tiles a CTA has at most); with mma.sync and the keys in
+// registers 66 us, bound by fragment loads.
 //   warps 0-3 / 4-7  epilogue of the even / odd (head, column group) items
 //   warp 8           TMA producer (K ring, Q ring);  warp 9  MMA issuer, TMEM owner
 // Four score tiles of 128 TMEM columns; the two halves' sums meet in shared memory.
@@ -20,8 +21,8 @@
 #include <algorithm>
 
 #include "kf_evict.cuh"
-#include "kf_mq_tc05.cuh"
 #include "kf_runs.cuh"
+#include "kf_tc05_ops.cuh"
 
 namespace kf {
 namespace {
@@ -196,7 +197,7 @@ accumulate_tc05_kernel(const AccumulateParams p, const __grid_constant__ CUtenso
                     const int N = min(kCols, (cols - c0 + 15) & ~15);
                     const uint32_t id = tc05::idesc_bf16(kTok, N, false, false);
                     const uint64_t qd = tc05::sdesc_sw128(sQ + qs * Sh::kQBytes, 16, 1024);
-                    if (elect_one()) {
+                    if (tc05::elect_one()) {
 #pragma unroll
                         for (int kk = 0; kk < D / 16; ++kk)
                             tc05::mma_ss(tm + kCols * sb, kd + (uint64_t)(((kk >> 2) * 1024 + 32 * (kk & 3)) / 16),
@@ -210,7 +211,7 @@ accumulate_tc05_kernel(const AccumulateParams p, const __grid_constant__ CUtenso
                 }
             }
         });
-        if (elect_one()) {
+        if (tc05::elect_one()) {
             if (!ok) {
                 raise_error(p.err, KF_DEVERR_TIMEOUT);
                 abort_flag = 1;

@@ -15,6 +15,7 @@
 #include <queue>
 #include <vector>
 
+#include "kf_device.cuh"
 #include "kf_internal.cuh"
 
 namespace kf {

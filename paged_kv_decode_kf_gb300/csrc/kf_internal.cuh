@@ -98,11 +98,6 @@ cudaError_t launch_decode_step_bal_fp8(const DecodeParams &p, const StepArgs &a,
 // One bounded wait that nothing completes (sets KF_DEVERR_TIMEOUT).
 cudaError_t launch_wait_check(unsigned int *err, cudaStream_t stream);
 
-// Facts of the current device (set up on first use): its error word and SM
-// count; and cuTensorMapEncodeTiled (null if the driver has none).
-cudaError_t device_facts(unsigned int **err, int *sm_count);
-void *tensor_map_encoder();
-
 // Process-unique id of the CUDA context current on the calling thread (0 if
 // none): device addresses looked up in one context are stale in the next.
 unsigned long long current_context_id();

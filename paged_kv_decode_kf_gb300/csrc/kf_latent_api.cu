@@ -5,6 +5,7 @@
 
 #include <algorithm>
 
+#include "kf_device.cuh"
 #include "kf_evict.cuh"
 #include "kf_latent.cuh"
 

@@ -201,10 +201,10 @@ expand_kernel(const LatentParams p, const ExpandedKV kv, const __grid_constant__
                     mbar_arrive_expect_tx(full(st), Sh::kSliceBytes);
                     const uint32_t dst = sW + st * Sh::kSliceBytes;
                     if (Sh::kUnits == 2) {  // W_uk_h, W_uv_h in turn
-                        tma_load_3d(dst, (w.u & 1) ? &tmap_uv : &tmap_uk, 0, (w.u >> 1) * DN, a, full(st));
+                        tc05::tma_load_3d(dst, (w.u & 1) ? &tmap_uv : &tmap_uk, 0, (w.u >> 1) * DN, a, full(st));
                     } else {
-                        tma_load_3d(dst, &tmap_uk, 0, w.u * DN, a, full(st));
-                        tma_load_3d(dst + DN * 128, &tmap_uv, 0, w.u * DV, a, full(st));
+                        tc05::tma_load_3d(dst, &tmap_uk, 0, w.u * DN, a, full(st));
+                        tc05::tma_load_3d(dst + DN * 128, &tmap_uv, 0, w.u * DV, a, full(st));
                     }
                 }
             }
@@ -238,7 +238,7 @@ expand_kernel(const LatentParams p, const ExpandedKV kv, const __grid_constant__
                 ok = warp_wait(full(st), (g / NS) & 1);
                 if (!ok) break;
                 tc05::fence_after_sync();
-                if (elect_one()) {
+                if (tc05::elect_one()) {
 #pragma unroll
                     for (int kk = 0; kk < 4; ++kk)
                         tc05::mma_ss(tm + (u & 3) * kN, ad + (uint64_t)((a * 1024 + 32 * kk) / 16),
@@ -250,7 +250,7 @@ expand_kernel(const LatentParams p, const ExpandedKV kv, const __grid_constant__
             }
             if (!ok) break;
             const bool more = w.step(p, fresh);
-            if (elect_one()) {
+            if (tc05::elect_one()) {
                 tc05::commit(acc_full(u & 3));
                 if (!more || fresh) tc05::commit(a_empty);
             }
@@ -258,7 +258,7 @@ expand_kernel(const LatentParams p, const ExpandedKV kv, const __grid_constant__
             ++u;
             if (!more) break;
         } while (true);
-        if (elect_one()) {
+        if (tc05::elect_one()) {
             if (!ok) {
                 raise_error(p.err, KF_DEVERR_TIMEOUT);
                 abort_flag = 1;

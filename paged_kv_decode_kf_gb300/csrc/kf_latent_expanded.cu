@@ -179,8 +179,8 @@ expanded_kernel(const LatentParams p, const ExpandedKV kv, int q_tiles, const __
                 go = !abort_flag && mbar_wait(empty(st), ((j / NS) & 1) ^ 1);
                 if (go) {
                     mbar_arrive_expect_tx(full(st), (Sh::kKAtoms + DV / 64) * Sh::kAtomBytes + nblk * rope_bytes);
-                    tma_load_3d(sKV + st * Sh::kStageBytes, &tmap_k, 0, (int)(ws_row + t0), 0, full(st));
-                    tma_load_3d(sKV + st * Sh::kStageBytes + Sh::kVAt, &tmap_v, 0, (int)(ws_row + t0), 0, full(st));
+                    tc05::tma_load_3d(sKV + st * Sh::kStageBytes, &tmap_k, 0, (int)(ws_row + t0), 0, full(st));
+                    tc05::tma_load_3d(sKV + st * Sh::kStageBytes + Sh::kVAt, &tmap_v, 0, (int)(ws_row + t0), 0, full(st));
                 } else {
                     raise_error(p.err, KF_DEVERR_TIMEOUT);
                     abort_flag = 1;
@@ -219,7 +219,7 @@ expanded_kernel(const LatentParams p, const ExpandedKV kv, int q_tiles, const __
                     ok = warp_wait(p_full(t), (j - 1) & 1);
                     if (!ok) break;
                     tc05::fence_after_sync();
-                    if (elect_one()) {
+                    if (tc05::elect_one()) {
 #pragma unroll
                         for (int kk = 0; kk < kTok / 16; ++kk)
                             tc05::mma_ts(tm + Sh::col_o(t), s + 8 * kk, vd + (uint64_t)(kk * 2048 / 16), id_o,
@@ -236,7 +236,7 @@ expanded_kernel(const LatentParams p, const ExpandedKV kv, int q_tiles, const __
                 }
                 if (has_s) {
                     const uint64_t qd = tc05::sdesc_sw128(sQ + t * kRows * 128, 16, 1024);
-                    if (elect_one()) {
+                    if (tc05::elect_one()) {
 #pragma unroll
                         for (int kk = 0; kk < 2 * DN / 16; ++kk)  // q_n against hi, then against lo
                             tc05::mma_ts(s, q + 8 * (kk % (DN / 16)),
@@ -252,7 +252,7 @@ expanded_kernel(const LatentParams p, const ExpandedKV kv, int q_tiles, const __
                 }
             }
         }
-        if (elect_one()) {
+        if (tc05::elect_one()) {
             if (!ok) {
                 raise_error(p.err, KF_DEVERR_TIMEOUT);
                 abort_flag = 1;

@@ -9,8 +9,8 @@
 #pragma once
 
 #include "kf_latent.cuh"
-#include "kf_mq_tc05.cuh"
 #include "kf_runs.cuh"
+#include "kf_tc05_ops.cuh"
 
 namespace kf {
 

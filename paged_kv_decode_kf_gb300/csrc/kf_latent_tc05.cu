@@ -43,8 +43,8 @@
 // Every wait is bounded; one that gives up sets KF_DEVERR_TIMEOUT and the CTA
 // drains its copies and MMAs, frees its TMEM and returns.
 #include "kf_latent.cuh"
-#include "kf_mq_tc05.cuh"
 #include "kf_runs.cuh"
+#include "kf_tc05_ops.cuh"
 
 #include <algorithm>
 
@@ -334,7 +334,7 @@ latent_kernel(const LatentParams p, const Partials part, const __grid_constant__
     // an issuing warp's end: report a wait that gave up, and see every MMA issued done
     // before TMEM is freed
     auto finish = [&](bool ok, uint32_t bar) {
-        if (elect_one()) {
+        if (tc05::elect_one()) {
             if (!ok) {
                 raise_error(p.err, KF_DEVERR_TIMEOUT);
                 abort_flag = 1;
@@ -386,7 +386,7 @@ latent_kernel(const LatentParams p, const Partials part, const __grid_constant__
                         if (go) {
                             ++q_loads;
                             mbar_arrive_expect_tx(q_full, Sh::kQBytes);
-                            tma_load_3d(sQ, &tmap_q, 0, (int)(s.q0 * p.num_heads + s.row0), 0, q_full);
+                            tc05::tma_load_3d(sQ, &tmap_q, 0, (int)(s.q0 * p.num_heads + s.row0), 0, q_full);
                         }
                     }
                     if (go) mbar_arrive_expect_tx(full(st), nbox * 2 * Sh::kGroupBytes);
@@ -432,7 +432,7 @@ latent_kernel(const LatentParams p, const Partials part, const __grid_constant__
                 if (!ok) break;
                 tc05::fence_after_sync();
                 const uint64_t xd = tc05::sdesc_sw128(sX + st * Sh::kTileBytes, 16, Sh::kGroupBytes);
-                if (elect_one()) {
+                if (tc05::elect_one()) {
 #pragma unroll
                     for (int kk = 0; kk < KS; ++kk)
                         tc05::mma_ss(tm + Sh::kColS + 64 * sb,
@@ -465,7 +465,7 @@ latent_kernel(const LatentParams p, const Partials part, const __grid_constant__
                 if (!ok) break;
                 tc05::fence_after_sync();
                 const uint64_t cd = tc05::sdesc_sw128(sX + st * Sh::kTileBytes, 1024, Sh::kGroupBytes);
-                if (elect_one()) {
+                if (tc05::elect_one()) {
                     // (one accumulator after the other: alternating between them costs a fifth)
 #pragma unroll
                     for (int d = 0; d < Sh::kDimTiles; ++d)
