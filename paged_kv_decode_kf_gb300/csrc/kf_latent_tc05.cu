@@ -7,10 +7,11 @@
 // so one tile of X in shared memory serves both products: keys as they are, values
 // as the same bytes read along the other axis.
 //
-// Work. Rows come in tiles of 64 (R = 512) or 128 (R = 256), tokens in tiles of 64. A unit is one row tile of
-// one request over all its token tiles; the units of the batch, laid end to end,
-// are cut into equal runs, one a CTA (one CTA an SM: the tile ring fills its
-// shared memory). A run may start and end inside a unit; the parts of such a unit
+// Work. Rows come in tiles of 64 (R = 512) or 128 (R = 256), tokens in tiles of 64. A
+// unit is one row tile of one request over all its token tiles; the units of the
+// batch, laid end to end, are cut into equal runs, one a CTA (one CTA an SM: the
+// tile ring fills its shared memory); where requests have several units, one a pair
+// of CTAs, which walk it side by side. A run may start and end inside a unit; the parts of such a unit
 // go to the workspace as normalised (o, lse) partials and latent_merge joins
 // them. So a batch of any length mix keeps every SM busy to the end, at the
 // price of at most two partials a CTA.
@@ -25,18 +26,22 @@
 // shrinks with the rows. P goes through shared memory as that product's B.
 //   warps 0-3  softmax; 64-row tiles: rows 16 w .. 16 w + 15, four lanes a row (16x256b
 //              TMEM loads: lane l holds columns 8 i + 2 (l % 4), + 1 of rows l / 4 and
-//              l / 4 + 8); 128-row tiles: a thread a row. Base-2 online softmax with a lazy maximum (it moves only by more
-//              than 8, and then O^T's columns are rescaled in TMEM); the epilogue.
+//              l / 4 + 8); 128-row tiles: a thread a row. Base-2 online softmax with a
+//              lazy maximum (it moves only by more than 8, and then O^T's columns are
+//              rescaled in TMEM); the epilogue.
 //   warp 4     TMA producer;  warp 5  issues S and owns TMEM;  warp 6  issues O^T.
 // Score tiles alternate between two TMEM buffers, and the two products have an issuing
 // warp each: S of tile g + 1 goes out as soon as its tile has landed, the value
 // product of tile g as soon as its weights are there, whichever comes first.
 //
 // What bounds it: 2 (R + 64) bytes of cache a token. At R = 512 an SM's share of HBM
-// brings a token in 53 cycles (64 tokens x 1152 B at 44.6 B/ns); the instructions
-// take 26 (M = 64 runs at half rate) and shared memory 40 (fill, Q and X for S, C
-// and P for O), so up to 64 rows the cache is the bound; each further 64 rows
-// read the tile again, from L2.
+// brings a tile of 64 tokens in 3400 cycles (73.7 KB at 44.6 B/ns); its instructions
+// take 2070 (36 S instructions of 36 cycles, 16 O^T ones of 48) and shared memory 2500
+// (fill, Q and X for S, C and P for O), so up to 64 rows the cache is the bound: 16
+// requests of 8K-256K tokens and 32 heads run at 3340 cycles a tile (200 us, 0.81 of
+// the copy bandwidth with start, epilogues and merge). With more rows the two-slot
+// ring's latency is: load (1650) + S (1300-1800) + softmax (1100) + O^T (800-1050)
+// + hand-offs, over two slots.
 //
 // Tokens past a unit's last visible one are masked by selection (never multiplied)
 // and their rows zeroed in shared memory (0 * NaN would poison the product).
@@ -101,9 +106,11 @@ __device__ __forceinline__ Request request_of(const LatentParams &p, int b, bool
     return q;
 }
 
-__device__ __forceinline__ int64_t cost_of(const LatentParams &p, int b, bool report) {
+// Tiles of a request in the list that the runs are cut from: with `twins` = 2, two CTAs
+// share a run, one the even, one the odd units, tile by tile at the same time.
+__device__ __forceinline__ int64_t cost_of(const LatentParams &p, int b, int twins, bool report) {
     const Request r = request_of(p, b, report);
-    return r.n * r.units;
+    return r.n * ((r.units + twins - 1) / twins);
 }
 
 // One unit's part in a CTA's run: token tiles [tile0, tile0 + tiles).
@@ -120,6 +127,7 @@ struct Segment {
 struct Walker {
     Place at;
     int64_t pos, left;  // the next tile in the batch's list; tiles left of the run
+    int twins, twin;  // CTAs that share the run; which of them this is
     bool first = true;
     Request r;
     bool loaded = false;
@@ -130,15 +138,23 @@ struct Walker {
                 r = request_of(p, at.b, false);
                 loaded = true;
             }
-            if (at.off >= r.n * r.units) {  // on to the next request (some have no units)
+            const int64_t groups = (r.units + twins - 1) / twins;
+            if (at.off >= r.n * groups) {  // on to the next request (some have no units)
                 ++at.b;
                 at.off = 0;
                 loaded = false;
                 if (at.b >= p.batch) return false;
                 continue;
             }
-            const int64_t unit = at.off / r.n, tile = at.off - unit * r.n;
+            const int64_t group = at.off / r.n, tile = at.off - group * r.n;
             const int64_t len = left < r.n - tile ? left : r.n - tile;
+            const int64_t unit = group * twins + twin;
+            if (unit >= r.units) {  // the other twin's unit is the request's last
+                at.off += len;
+                pos += len;
+                left -= len;
+                continue;
+            }
             s.q0 = r.q0;
             const int M = unit_rows(p.latent_dim);
             s.row0 = unit * M;
@@ -170,11 +186,11 @@ struct Walker {
     }
 };
 
-// A unit cut over CTAs first .. first + parts - 1: where its partials lie. The first
-// CTA's slot is `slot0`; the others' is the first of their two (2 i).
+// A unit cut over the CTAs i, i + twins, i + 2 twins, ...: where its partials lie. The
+// first CTA's slot is `slot0`; the others' is the first of their two (2 i).
 struct Cut {
     int64_t row_out;  // its first row in out and lse_out
-    int rows, parts, slot0, pad;
+    int rows, parts, slot0, twins;
 };
 
 struct Partials {
@@ -273,7 +289,7 @@ __device__ __forceinline__ void store_rows(uint32_t tm, bool any, int rows, cons
 // ---------------------------------------------------------------------------
 template <int R>
 __global__ void __launch_bounds__(kThreads, 1)
-latent_kernel(const LatentParams p, const Partials part, const __grid_constant__ CUtensorMap tmap_x,
+latent_kernel(const LatentParams p, const Partials part, int twins, const __grid_constant__ CUtensorMap tmap_x,
               const __grid_constant__ CUtensorMap tmap_q) {
     using Sh = LShape<R>;
     constexpr int NS = Sh::kStages, KS = (R + kRopeDim) / 16, KP = kN / 16, kM = Sh::kM;
@@ -318,13 +334,16 @@ latent_kernel(const LatentParams p, const Partials part, const __grid_constant__
     // what ran before on the stream (an append, say) is complete from here on
     asm volatile("griddepcontrol.wait;" ::: "memory");
     if (threadIdx.x == 0) abort_flag = (*(volatile unsigned int *)p.err & KF_DEVERR_TIMEOUT) ? 1 : 0;
+    const int run = blockIdx.x / twins, runs = gridDim.x / twins;
     Walker walk;
+    walk.twins = twins;
+    walk.twin = blockIdx.x - run * twins;
     int64_t slot0;
     const int64_t total = locate(
-        p.batch, [&](int b) { return cost_of(p, b, blockIdx.x == 0); }, sm_loc,
-        [&](int64_t T) { return cut_at(blockIdx.x, gridDim.x, T); }, walk.at, slot0);
+        p.batch, [&](int b) { return cost_of(p, b, twins, blockIdx.x == 0); }, sm_loc,
+        [&](int64_t T) { return cut_at(run, runs, T); }, walk.at, slot0);
     walk.pos = slot0;
-    walk.left = cut_at(blockIdx.x + 1, gridDim.x, total) - slot0;
+    walk.left = cut_at(run + 1, runs, total) - slot0;
     if (abort_flag) walk.left = 0;  // an earlier kernel's wait gave up (no role has started yet)
     tc05::fence_before_sync();
     __syncthreads();
@@ -662,9 +681,9 @@ latent_kernel(const LatentParams p, const Partials part, const __grid_constant__
             const int64_t slot = 2 * (int64_t)blockIdx.x + (s.first ? 0 : 1);
             const int64_t row_out = s.q0 * p.num_heads + s.row0;
             if (s.cut) {
-                const int64_t P = (int64_t)gridDim.x < total ? gridDim.x : total;
-                const int64_t last = (s.unit_end * P - 1) / total;  // the CTA of the unit's last tile
-                cut = Cut{row_out, s.rows, (int)(last - blockIdx.x) + 1, (int)slot, 0};
+                const int64_t P = runs < total ? runs : total;
+                const int64_t last = (s.unit_end * P - 1) / total;  // the run of the unit's last tile
+                cut = Cut{row_out, s.rows, (int)(last - run) + 1, (int)slot, twins};
             }
             if (s.tiles > 0) tc05::fence_after_sync();
             // O^T: thread = column, one row a TMEM column; 32 consecutive numbers a warp and store
@@ -722,7 +741,7 @@ latent_merge_kernel(const LatentParams p, const Partials part) {
     const Cut cut = part.cuts[blockIdx.x];
     const int n = cut.parts, rows = cut.rows;
     if (n == 0 || blockIdx.y * RPB >= rows) return;
-    auto slot_at = [&](int i) { return i == 0 ? (int64_t)cut.slot0 : 2 * ((int64_t)blockIdx.x + i); };
+    auto slot_at = [&](int i) { return i == 0 ? (int64_t)cut.slot0 : 2 * ((int64_t)blockIdx.x + i * cut.twins); };
     const int sub = warp % WPR;
     const int row = blockIdx.y * RPB + warp / WPR;
     const bool live = row < rows;
@@ -823,7 +842,7 @@ bool encode_cache(tc::EncodeFn fn, CUtensorMap *map, const LatentParams &p) {
 }
 
 template <int R>
-cudaError_t launch(const LatentParams &p, const Partials &part, int ctas, bool long_units, cudaStream_t stream,
+cudaError_t launch(const LatentParams &p, const Partials &part, int ctas, int twins, bool long_units, cudaStream_t stream,
                    const CUtensorMap &mx, const CUtensorMap &mq) {
     using Sh = LShape<R>;
     static std::atomic<uint64_t> done{0};
@@ -847,15 +866,15 @@ cudaError_t launch(const LatentParams &p, const Partials &part, int ctas, bool l
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    e = cudaLaunchKernelEx(&cfg, latent_kernel<R>, p, part, mx, mq);
-    if (e != cudaSuccess || ctas == 1) return e;
+    e = cudaLaunchKernelEx(&cfg, latent_kernel<R>, p, part, twins, mx, mq);
+    if (e != cudaSuccess || ctas == twins) return e;
     cfg.blockDim = dim3(256);
     cfg.dynamicSmemBytes = 0;
     if (long_units) {
-        cfg.gridDim = dim3(ctas - 1, part.pitch);
+        cfg.gridDim = dim3(ctas - twins, part.pitch);
         return cudaLaunchKernelEx(&cfg, latent_merge_kernel<R, 1>, p, part);
     }
-    cfg.gridDim = dim3(ctas - 1, (part.pitch + 7) / 8);
+    cfg.gridDim = dim3(ctas - twins, (part.pitch + 7) / 8);
     return cudaLaunchKernelEx(&cfg, latent_merge_kernel<R, 8>, p, part);
 }
 
@@ -866,19 +885,27 @@ size_t al256(size_t x) { return (x + 255) & ~(size_t)255; }
 }  // namespace
 
 size_t latent_workspace_bytes(int batch, int max_query_len, int num_heads, int latent_dim, int sm_count) {
+    sm_count = std::max(sm_count, 2);
     const size_t rows = 2 * (size_t)sm_count * row_pitch(max_query_len, num_heads, latent_dim);
     return al256(rows * latent_dim * 4) + al256(rows * 4) + sm_count * sizeof(Cut);
 }
 
 cudaError_t launch_latent(const LatentParams &p, void *workspace, int sm_count, cudaStream_t stream, void *encode_fn) {
     tc::EncodeFn fn = reinterpret_cast<tc::EncodeFn>(encode_fn);
+    sm_count = std::max(sm_count, 2);
     CUtensorMap mx, mq;
     if (!encode_cache(fn, &mx, p) || !encode_q(fn, &mq, p)) return cudaErrorInvalidValue;
     // no more CTAs than the batch can have tiles
+    // Requests of more than one unit: two CTAs walk a run together, a unit each, so that
+    // one's tiles are the other's L2 hits (64 requests of 4K tokens, 128 heads: 303 MB
+    // read from HBM instead of 550). With one unit a request there is nothing to share.
     const int M = unit_rows(p.latent_dim);
-    const int64_t units = (int64_t)p.batch * (((int64_t)p.max_query_len * p.num_heads + M - 1) / M);
-    const int64_t tiles = units * std::max<int64_t>(1, ((int64_t)p.max_context_len + kN - 1) / kN);
-    const int ctas = (int)std::min<int64_t>(sm_count, tiles);
+    const int64_t rows_max = (int64_t)p.max_query_len * p.num_heads;
+    const int twins = rows_max > M ? 2 : 1;
+    // no more runs than the batch can have tiles
+    const int64_t groups = (int64_t)p.batch * ((rows_max + twins * M - 1) / (twins * M));
+    const int64_t tiles = groups * std::max<int64_t>(1, ((int64_t)p.max_context_len + kN - 1) / kN);
+    const int ctas = twins * (int)std::min<int64_t>(std::max(1, sm_count / twins), tiles);
     Partials part;
     part.pitch = (int)row_pitch(p.max_query_len, p.num_heads, p.latent_dim);
     part.o = static_cast<float *>(workspace);
@@ -888,9 +915,9 @@ cudaError_t launch_latent(const LatentParams &p, void *workspace, int sm_count, 
     part.cuts = reinterpret_cast<Cut *>(ws + al256(rows * 4));
     // few units are cut over many CTAs each: one row a merge block, its warps share
     // the partials; many units have two or three partials: one warp a row
-    const bool long_units = units * 8 < ctas;
-    return p.latent_dim == 512 ? launch<512>(p, part, ctas, long_units, stream, mx, mq)
-                               : launch<256>(p, part, ctas, long_units, stream, mx, mq);
+    const bool long_units = groups * twins * 8 < ctas;
+    return p.latent_dim == 512 ? launch<512>(p, part, ctas, twins, long_units, stream, mx, mq)
+                               : launch<256>(p, part, ctas, twins, long_units, stream, mx, mq);
 }
 
 }  // namespace kf
