@@ -422,7 +422,8 @@ template <int D, bool KV8>
 cudaError_t launch(const AccumulateParams &p, int sm_count, cudaStream_t stream, void *encode_fn) {
     // Columns a KV head: up to eight are one pass of the row kernel; more keep the keys
     // while the columns pass, bf16 ones on tcgen05 (E4M3 keys need fp16 products, and
-    // tcgen05 takes no fp16 operand beside an 8-bit one).
+    // tcgen05 takes no fp16 operand beside an 8-bit one). 64 requests of 4K tokens, 8 / 16
+    // / 32 columns: 94 / 110 / 152 us with the row kernel, 106 / 107 / 107 on tcgen05.
     const int64_t cols = (int64_t)p.max_query_len * (p.num_q_heads / p.num_kv_heads);
     if (!KV8 && cols > 8 && p.num_q_tokens > 0) return launch_accumulate_tc05(p, sm_count, stream, encode_fn);
     const int64_t tiles = (int64_t)p.batch * ((p.max_context_len + 15) / 16);

@@ -17,12 +17,12 @@
 // One cluster of CL CTAs a request, each with a contiguous part of its tokens,
 // whose keys stay in shared memory from one global read on (up to 49152 a CTA;
 // beyond, every pass computes them again). Histograms and counts meet through
-// distributed shared memory, one cluster barrier a pass. CL = 1 up to 8192
-// tokens, where barriers across CTAs would cost more than they save; 8 above.
+// distributed shared memory, one cluster barrier a pass.
 //
 // What bounds it: 4 bytes a token to select (8 with positions), 2 row_bytes a moved
-// row and cache. The selection of a short request is latency: a chain of four
-// passes and two scans.
+// row and cache (8 requests of 64K-128K tokens cut to 12289, 12 K rows of 2 x 2 KB
+// moved at 6.9 TB/s: 102 us of 137). The selection is latency: a chain of four passes
+// and two scans, 12 us for 2K tokens, 30 for 128K.
 #include <algorithm>
 #include <atomic>
 
@@ -377,16 +377,29 @@ cudaError_t launch_select(const EvictParams &p, cudaStream_t stream) {
     return cudaLaunchKernelEx(&cfg, evict_select_kernel<CL, MOVE>, p, slots);
 }
 
+template <bool MOVE>
+cudaError_t launch_select(const EvictParams &p, int cl, cudaStream_t stream) {
+    switch (cl) {
+        case 1: return launch_select<1, MOVE>(p, stream);
+        case 2: return launch_select<2, MOVE>(p, stream);
+        case 4: return launch_select<4, MOVE>(p, stream);
+        default: return launch_select<8, MOVE>(p, stream);
+    }
+}
+
 }  // namespace
 
 cudaError_t launch_evict(const EvictParams &p, int sm_count, cudaStream_t stream) {
-    // a few moved rows a request are cheaper in the selecting CTA than in a launch of
-    // their own
-    const bool in_place = p.max_moves <= 64;
-    const bool wide = p.max_context_len > 8192;
-    cudaError_t e;
-    if (in_place) e = wide ? launch_select<8, true>(p, stream) : launch_select<1, true>(p, stream);
-    else e = wide ? launch_select<8, false>(p, stream) : launch_select<1, false>(p, stream);
+    // A warp a row in the selecting CTA while it has one for each, else a launch of their
+    // own (8 requests of 4K tokens, rows of 2 x 2 KB: 1 / 16 / 64 / 256 moves take 14.5 /
+    // 16.5 / 19.9 / 34.9 us in the CTA, 16.5 / 18.3 / 18.2 / 18.6 in a launch).
+    const bool in_place = p.max_moves <= 32;
+    // CTAs a request: doubled while each has more than 6144 tokens, and the batch stays one
+    // wave (4 requests of 4K / 8K / 32K tokens: 14.5 / 18.6 / 43.1 us with one CTA, 16.6 /
+    // 16.5 / 20.6 with eight; 64 requests of 32K: 43.1 with one, 30.8 with two, 76 with eight).
+    int cl = 1;
+    while (cl < 8 && p.batch * cl * 2 <= sm_count && p.max_context_len > 6144 * cl) cl *= 2;
+    const cudaError_t e = in_place ? launch_select<true>(p, cl, stream) : launch_select<false>(p, cl, stream);
     if (e != cudaSuccess || in_place) return e;
     // at most some 4800 CTAs over the batch (a CTA for every eight possible moves was
     // 10000 CTAs, most of them empty, where 33 requests moved 300 rows each)

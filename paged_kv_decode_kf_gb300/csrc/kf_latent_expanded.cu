@@ -20,7 +20,10 @@
 // Tile 0's products run while tile 1's softmax does, and the other way round.
 //
 // What bounds it: the tensor pipe, 2 x 20 score and 2 x 4 value instructions a 64-token
-// stage, and beside it the softmax's exponentials.
+// stage: 2064 cycles of the 2450 a stage takes (4 requests, 1024 queries each at 4K-12K
+// tokens, 32 heads: 614 us, the pipe 68 % busy, with the last wave's tail). The rest is
+// the hand-off from a tile's softmax to its next products. An issuing warp a tile
+// instead of one for both let the tiles' instructions interleave: 12 % slower.
 //
 // Tokens past the last row's limit are masked by selection, and their V rows zeroed
 // in shared memory (0 * NaN). Every wait is bounded; one that gives up sets

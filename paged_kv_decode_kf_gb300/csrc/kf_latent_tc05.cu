@@ -897,8 +897,9 @@ cudaError_t launch_latent(const LatentParams &p, void *workspace, int sm_count, 
     if (!encode_cache(fn, &mx, p) || !encode_q(fn, &mq, p)) return cudaErrorInvalidValue;
     // no more CTAs than the batch can have tiles
     // Requests of more than one unit: two CTAs walk a run together, a unit each, so that
-    // one's tiles are the other's L2 hits (64 requests of 4K tokens, 128 heads: 303 MB
-    // read from HBM instead of 550). With one unit a request there is nothing to share.
+    // one's tiles are the other's L2 hits (64 requests of 4K tokens, 128 heads: 117 us
+    // against 130, which read 550 MB from HBM for a cache of 302). With one unit a
+    // request there is nothing to share.
     const int M = unit_rows(p.latent_dim);
     const int64_t rows_max = (int64_t)p.max_query_len * p.num_heads;
     const int twins = rows_max > M ? 2 : 1;
@@ -914,7 +915,8 @@ cudaError_t launch_latent(const LatentParams &p, void *workspace, int sm_count, 
     part.lse = reinterpret_cast<float *>(ws);
     part.cuts = reinterpret_cast<Cut *>(ws + al256(rows * 4));
     // few units are cut over many CTAs each: one row a merge block, its warps share
-    // the partials; many units have two or three partials: one warp a row
+    // the partials; many units have two or three partials: one warp a row (1 request of
+    // 30K tokens, 16 heads: 31 us against 77; 32 requests of 8K: 80 against 77)
     const bool long_units = groups * twins * 8 < ctas;
     return p.latent_dim == 512 ? launch<512>(p, part, ctas, twins, long_units, stream, mx, mq)
                                : launch<256>(p, part, ctas, twins, long_units, stream, mx, mq);
