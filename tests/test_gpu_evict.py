@@ -216,6 +216,7 @@ def test_evict_wide_and_few_moves(kf):
     _evict_case(kf, [9000, 8991, 8990, 100], 8990, 4, 100, 64, 2, True, 10)
     _evict_case(kf, [400001], 399990, 0, 5, 16, 1, False, 11)
     _evict_case(kf, [400001], 1000, 4, 5, 16, 1, False, 12)
+    _evict_case(kf, [20000, 300, 12289], 5000, 4, 50, 32, 1, True, 15)
 
 
 def test_evict_many_requests(kf):
