@@ -445,12 +445,12 @@ def kf_decode_step_fp8(q, k_new, v_new, k_cache, v_cache, k_scale, v_scale, bloc
     return out, lse_out
 
 
-def _latent_dims(latent_cache: torch.Tensor) -> Tuple[int, int, int, int]:
-    """(num_blocks, block_size, latent_dim, rope_dim) of a latent cache."""
-    if latent_cache.dim() != 3 or latent_cache.shape[2] <= KF_ROPE_DIM:
+def _latent_dims(latent_cache: torch.Tensor) -> Tuple[int, int, int]:
+    """(num_blocks, block_size, latent_dim) of a latent cache."""
+    shape = latent_cache.shape
+    if len(shape) != 3 or shape[2] <= KF_ROPE_DIM:
         raise ValueError("latent_cache must be [num_blocks, block_size, latent_dim + %d]" % KF_ROPE_DIM)
-    nb, bs, w = latent_cache.shape
-    return nb, bs, w - KF_ROPE_DIM, KF_ROPE_DIM
+    return shape[0], shape[1], shape[2] - KF_ROPE_DIM
 
 
 def _shape(t: torch.Tensor, shape, name: str) -> None:
@@ -479,11 +479,11 @@ def _call(name: str, index: int, stream, *args) -> None:
 
 def _on(index: int, t: torch.Tensor, dtype, name: str) -> int:
     """The address of a contiguous tensor of `dtype` on device `index`."""
-    if t.dtype != dtype or t.get_device() != index or not t.is_contiguous():
-        if t.get_device() != index:
-            raise ValueError("%s must be on the call's device, cuda:%d, got %s" % (name, index, t.device))
-        return _dev(t, dtype, name)   # names what is wrong
-    return t.data_ptr()
+    if t.dtype is dtype and t.get_device() == index and t.is_contiguous():
+        return t.data_ptr()
+    if t.get_device() != index:
+        raise ValueError("%s must be on the call's device, cuda:%d, got %s" % (name, index, t.device))
+    return _dev(t, dtype, name)   # names what is wrong
 
 
 def _opt(index: int, t: Optional[torch.Tensor], dtype, name: str) -> Optional[int]:
@@ -498,9 +498,10 @@ def kf_append_latent(latent_new: torch.Tensor, latent_cache: torch.Tensor, block
                      stream=None) -> None:
     """Write each request's new latent rows (one, or rows row_start[b]..row_start[b+1]-1)
     from position context_lens_before[b] on."""
-    nb, bs, r, rope = _latent_dims(latent_cache)
-    B, n = block_tables.shape[0], latent_new.shape[0]
-    _shape(latent_new, (n, r + rope), "latent_new")
+    nb, bs, r = _latent_dims(latent_cache)
+    B, columns = block_tables.shape
+    n = latent_new.shape[0]
+    _shape(latent_new, (n, r + KF_ROPE_DIM), "latent_new")
     _shape(context_lens_before, (B,), "context_lens_before")
     if row_start is not None:
         _shape(row_start, (B + 1,), "row_start")
@@ -508,9 +509,10 @@ def kf_append_latent(latent_new: torch.Tensor, latent_cache: torch.Tensor, block
         raise ValueError("latent_new must hold one row a request without row_start")
     dev = latent_cache.get_device()
     _call("kf_append_latent", dev, stream,
-          _on(dev, latent_new, torch.bfloat16, "latent_new"), _opt(dev, row_start, torch.int32, "row_start"),
+          _on(dev, latent_new, torch.bfloat16, "latent_new"),
+          None if row_start is None else _on(dev, row_start, torch.int32, "row_start"),
           _on(dev, latent_cache, torch.bfloat16, "latent_cache"), _on(dev, block_tables, torch.int32, "block_tables"),
-          block_tables.shape[1], _on(dev, context_lens_before, torch.int32, "context_lens_before"), B, n, r, rope, bs, nb)
+          columns, _on(dev, context_lens_before, torch.int32, "context_lens_before"), B, n, r, KF_ROPE_DIM, bs, nb)
 
 
 def kf_latent_workspace_size(batch: int, max_query_len: int, num_heads: int, latent_dim: int) -> int:
@@ -526,29 +528,33 @@ def make_latent_workspace(batch: int, max_query_len: int, num_heads: int, latent
         return torch.empty(max(n, 16), dtype=torch.uint8, device=dev)
 
 
-def _latent_call(q, width, out_width, block_tables, context_lens, q_start, out, out_dtype, lse_out, want_lse):
-    """Shape checks and outputs shared by the two forms; returns (out, out code, lse_out)."""
-    if q.dim() != 3:
-        raise ValueError("q must be [num_q_tokens, num_heads, %d]" % width)
-    nq, h, _ = q.shape
-    _shape(q, (nq, h, width), "q")
-    B = block_tables.shape[0]
-    _shape(context_lens, (B,), "context_lens")
+def _latent_call(q, width, out_width, B, context_lens, q_start, out, out_dtype, lse_out, want_lse):
+    """Shape checks and outputs shared by the two forms; returns (num_q_tokens,
+    num_heads, out, out code, lse_out)."""
+    shape = q.shape
+    if len(shape) != 3 or shape[2] != width:
+        raise ValueError("q must be [num_q_tokens, num_heads, %d], got %s" % (width, list(shape)))
+    nq, h, _ = shape
+    if context_lens.shape != (B,):
+        _shape(context_lens, (B,), "context_lens")
     if q_start is not None:
-        _shape(q_start, (B + 1,), "q_start")
+        if q_start.shape != (B + 1,):
+            _shape(q_start, (B + 1,), "q_start")
     elif nq != B:
         raise ValueError("q must hold one query token a request without q_start")
     if out is None:
         out = torch.empty((nq, h, out_width), dtype=out_dtype, device=q.device)
-    _shape(out, (nq, h, out_width), "out")
-    code = {torch.float32: KF_F32, torch.bfloat16: KF_BF16}.get(out.dtype)
-    if code is None:
+    elif out.shape != (nq, h, out_width):
+        _shape(out, (nq, h, out_width), "out")
+    dtype = out.dtype
+    if dtype is not torch.float32 and dtype is not torch.bfloat16:
         raise ValueError("out must be float32 or bfloat16")
-    if lse_out is None and want_lse:
-        lse_out = torch.empty((nq, h), dtype=torch.float32, device=q.device)
-    if lse_out is not None:
+    if lse_out is None:
+        if want_lse:
+            lse_out = torch.empty((nq, h), dtype=torch.float32, device=q.device)
+    elif lse_out.shape != (nq, h):
         _shape(lse_out, (nq, h), "lse_out")
-    return out, code, lse_out
+    return nq, h, out, KF_F32 if dtype is torch.float32 else KF_BF16, lse_out
 
 
 def kf_latent_attention(q: torch.Tensor, latent_cache: torch.Tensor, block_tables: torch.Tensor,
@@ -559,17 +565,18 @@ def kf_latent_attention(q: torch.Tensor, latent_cache: torch.Tensor, block_table
                         stream=None) -> Tuple[torch.Tensor, Optional[torch.Tensor]]:
     """Latent attention, absorbed form: q [Nq, H, R + 64] over the latent cache;
     returns (out [Nq, H, R], lse [Nq, H])."""
+    nb, bs, r = _latent_dims(latent_cache)
+    B, columns = block_tables.shape
+    nq, h, out, code, lse_out = _latent_call(q, r + KF_ROPE_DIM, r, B, context_lens, q_start, out, out_dtype, lse_out,
+                                             want_lse)
     dev = q.get_device()
-    nb, bs, r, rope = _latent_dims(latent_cache)
-    out, code, lse_out = _latent_call(q, r + rope, r, block_tables, context_lens, q_start, out, out_dtype, lse_out,
-                                      want_lse)
     _call("kf_latent_attention", dev, stream,
-          _on(dev, q, torch.bfloat16, "q"), _opt(dev, q_start, torch.int32, "q_start"),
+          _on(dev, q, torch.bfloat16, "q"), None if q_start is None else _on(dev, q_start, torch.int32, "q_start"),
           _on(dev, latent_cache, torch.bfloat16, "latent_cache"), _on(dev, block_tables, torch.int32, "block_tables"),
-          block_tables.shape[1], _on(dev, context_lens, torch.int32, "context_lens"), int(bool(causal)),
-          int(max_context_len), int(max_query_len), block_tables.shape[0], q.shape[0], q.shape[1], r, rope, bs, nb,
-          float(scale), _on(dev, workspace, torch.uint8, "workspace"), workspace.numel(), _on(dev, out, out.dtype, "out"),
-          code, _opt(dev, lse_out, torch.float32, "lse_out"))
+          columns, _on(dev, context_lens, torch.int32, "context_lens"), 1 if causal else 0,
+          int(max_context_len), int(max_query_len), B, nq, h, r, KF_ROPE_DIM, bs, nb, float(scale),
+          _on(dev, workspace, torch.uint8, "workspace"), workspace.numel(), _on(dev, out, out.dtype, "out"), code,
+          None if lse_out is None else _on(dev, lse_out, torch.float32, "lse_out"))
     return out, lse_out
 
 
@@ -595,56 +602,60 @@ def kf_latent_attention_expanded(q: torch.Tensor, latent_cache: torch.Tensor, w_
                                  want_lse: bool = True, stream=None) -> Tuple[torch.Tensor, Optional[torch.Tensor]]:
     """Latent attention, expanded form: q [Nq, H, Dn + 64], w_uk [H, Dn, R], w_uv
     [H, Dv, R]; returns (out [Nq, H, Dv], lse [Nq, H])."""
-    dev = q.get_device()
-    nb, bs, r, rope = _latent_dims(latent_cache)
+    nb, bs, r = _latent_dims(latent_cache)
     if w_uk.dim() != 3 or w_uv.dim() != 3:
         raise ValueError("w_uk and w_uv must be [num_heads, width, latent_dim]")
     dn, dv = w_uk.shape[1], w_uv.shape[1]
-    out, code, lse_out = _latent_call(q, dn + rope, dv, block_tables, context_lens, q_start, out, out_dtype, lse_out,
-                                      want_lse)
-    _shape(w_uk, (q.shape[1], dn, r), "w_uk")
-    _shape(w_uv, (q.shape[1], dv, r), "w_uv")
+    B, columns = block_tables.shape
+    nq, h, out, code, lse_out = _latent_call(q, dn + KF_ROPE_DIM, dv, B, context_lens, q_start, out, out_dtype,
+                                             lse_out, want_lse)
+    _shape(w_uk, (h, dn, r), "w_uk")
+    _shape(w_uv, (h, dv, r), "w_uv")
+    dev = q.get_device()
     _call("kf_latent_attention_expanded", dev, stream,
-          _on(dev, q, torch.bfloat16, "q"), _opt(dev, q_start, torch.int32, "q_start"),
+          _on(dev, q, torch.bfloat16, "q"), None if q_start is None else _on(dev, q_start, torch.int32, "q_start"),
           _on(dev, latent_cache, torch.bfloat16, "latent_cache"), _on(dev, w_uk, torch.bfloat16, "w_uk"),
-          _on(dev, w_uv, torch.bfloat16, "w_uv"), _on(dev, block_tables, torch.int32, "block_tables"),
-          block_tables.shape[1], _on(dev, context_lens, torch.int32, "context_lens"), int(bool(causal)),
-          int(max_context_len), int(max_query_len), block_tables.shape[0], q.shape[0], q.shape[1], r, rope, dn, dv,
-          bs, nb, float(scale), _on(dev, workspace, torch.uint8, "workspace"), workspace.numel(),
-          _on(dev, out, out.dtype, "out"), code, _opt(dev, lse_out, torch.float32, "lse_out"))
+          _on(dev, w_uv, torch.bfloat16, "w_uv"), _on(dev, block_tables, torch.int32, "block_tables"), columns,
+          _on(dev, context_lens, torch.int32, "context_lens"), 1 if causal else 0, int(max_context_len),
+          int(max_query_len), B, nq, h, r, KF_ROPE_DIM, dn, dv, bs, nb, float(scale),
+          _on(dev, workspace, torch.uint8, "workspace"), workspace.numel(), _on(dev, out, out.dtype, "out"), code,
+          None if lse_out is None else _on(dev, lse_out, torch.float32, "lse_out"))
     return out, lse_out
 
 
 def _accumulate(name, q, k_cache, k_scale, block_tables, context_lens, max_context_len, scale, lse, scores_out,
                 scores_in, q_start, max_query_len, causal, stream):
-    dev = q.get_device()
     nq, hq, d = q.shape
-    nb, bs, hkv, _ = k_cache.shape
-    _shape(k_cache, (nb, bs, hkv, d), "k_cache")
-    B = block_tables.shape[0]
+    nb, bs, hkv, kd = k_cache.shape
+    if kd != d:
+        _shape(k_cache, (nb, bs, hkv, d), "k_cache")
+    B, columns = block_tables.shape
     _shape(context_lens, (B,), "context_lens")
     _shape(lse, (nq, hq), "lse")
-    if scores_out.dim() != 2 or scores_out.shape[0] != B:
+    out_shape = scores_out.shape
+    if len(out_shape) != 2 or out_shape[0] != B:
         raise ValueError("scores_out must be [batch, stride]")
     if scores_in is not None:
-        _shape(scores_in, scores_out.shape, "scores_in")
+        _shape(scores_in, out_shape, "scores_in")
     if q_start is not None:
         _shape(q_start, (B + 1,), "q_start")
     elif nq != B:
         raise ValueError("q must hold one query token a request without q_start")
-    if k_scale is not None:
+    dev = q.get_device()
+    if k_scale is None:
+        keys = (_on(dev, k_cache, torch.bfloat16, "k_cache"),)
+    else:
         _shape(k_scale, (hkv,), "k_scale")
-    if k_scale is not None and k_cache.get_device() != dev:
-        raise ValueError("k_cache must be on the call's device, cuda:%d, got %s" % (dev, k_cache.device))
-    cache = _on(dev, k_cache, torch.bfloat16, "k_cache") if k_scale is None else _dev8(k_cache, "k_cache")
-    scales = () if k_scale is None else (_on(dev, k_scale, torch.float32, "k_scale"),)
+        if k_cache.get_device() != dev:
+            raise ValueError("k_cache must be on the call's device, cuda:%d, got %s" % (dev, k_cache.device))
+        keys = (_dev8(k_cache, "k_cache"), _on(dev, k_scale, torch.float32, "k_scale"))
     _call(name, dev, stream,
-          _on(dev, q, torch.bfloat16, "q"), _opt(dev, q_start, torch.int32, "q_start"), cache, *scales,
-          _on(dev, block_tables, torch.int32, "block_tables"), block_tables.shape[1],
-          _on(dev, context_lens, torch.int32, "context_lens"), int(bool(causal)), int(max_context_len),
+          _on(dev, q, torch.bfloat16, "q"), None if q_start is None else _on(dev, q_start, torch.int32, "q_start"),
+          *keys, _on(dev, block_tables, torch.int32, "block_tables"), columns,
+          _on(dev, context_lens, torch.int32, "context_lens"), 1 if causal else 0, int(max_context_len),
           int(max_query_len), B, nq, hq, hkv, d, bs, nb, float(scale), _on(dev, lse, torch.float32, "lse"),
-          _opt(dev, scores_in, torch.float32, "scores_in"), _on(dev, scores_out, torch.float32, "scores_out"),
-          scores_out.shape[1])
+          None if scores_in is None else _on(dev, scores_in, torch.float32, "scores_in"),
+          _on(dev, scores_out, torch.float32, "scores_out"), out_shape[1])
     return scores_out
 
 

@@ -255,6 +255,52 @@ def test_absorbed_graph(kf):
         c.check(out.cpu(), lse.cpu())
 
 
+def test_absorbed_graph_after_copies_and_a_joined_stream(kf):
+    """The call directly behind copies, from the device and from pinned memory, and
+    behind an event of another stream: captured, it still waits for all of them."""
+    c = Case([100, 31, 640], [1, 1, 1], 16, 512, seed=30)
+    q, cache, table, ctx, qs = c.dev()
+    ws = kf.make_latent_workspace(3, 1, 16, 512)
+    out = torch.zeros(3, 16, 512, device="cuda")
+    lse = torch.zeros(3, 16, device="cuda")
+    src, rows = torch.empty_like(q), torch.empty_like(cache)
+    pinned = torch.empty(q.shape, dtype=q.dtype).pin_memory()
+    side = torch.cuda.Stream()
+
+    def step(kind):
+        if kind == "device":
+            q.copy_(src)
+        elif kind == "pinned":
+            q.copy_(pinned, non_blocking=True)
+        else:
+            side.wait_stream(torch.cuda.current_stream())
+            with torch.cuda.stream(side):
+                cache.copy_(rows)
+            torch.cuda.current_stream().wait_stream(side)
+        kf.kf_latent_attention(q, cache, table, ctx, c.max_ctx, c.scale, ws, out=out, lse_out=lse)
+
+    for kind in ("device", "pinned", "joined"):
+        rows.copy_(cache)
+        src.copy_(q)
+        pinned.copy_(q)
+        step(kind)
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            step(kind)
+        for seed in (1, 2):
+            gen = torch.Generator().manual_seed(seed)
+            new = torch.randn(q.shape, generator=gen).to(torch.bfloat16)
+            src.copy_(new)
+            pinned.copy_(new)
+            rows.copy_(torch.randn(cache.shape, generator=gen).to(torch.bfloat16))
+            torch.cuda.synchronize()
+            g.replay()
+            torch.cuda.synchronize()
+            c.q, c.cache = q.cpu(), cache.cpu()
+            c.check(out.cpu(), lse.cpu())
+
+
 @pytest.mark.parametrize("R", [512, 256])
 def test_absorbed_more_queries_than_tokens(kf, R):
     """C > L, causal: the first C - L queries see nothing."""
