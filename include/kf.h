@@ -468,8 +468,9 @@ kf_status kf_decode_step_static(const void *q, const void *k_new, const void *v_
  *    chunk of about 170 queries on at latent_dim 512, nope_dim = v_dim = 128).
  *
  * Shapes: latent_dim 256 or 512, rope_dim 64, block_size 16 or 32, num_heads
- * from 1 to 1024. Conventions, errors and device errors as the other calls
- * (host pointers are not taken); every device pointer is 16-byte aligned but
+ * from 1 to 1024, at most 2^30 tokens a request (KF_ERR_UNSUPPORTED above).
+ * Conventions, errors and device errors as the other calls (host pointers are
+ * not taken); every device pointer is 16-byte aligned but
  * for int32 and f32 arrays of one element per row, table entry or request,
  * which need 4 bytes.
  */
@@ -523,8 +524,9 @@ kf_status kf_append_latent(const void *latent_new, const int32_t *row_start, voi
  * bf16 (the cache's type), the sum that normalises them does not.
  * Host errors as kf_paged_multiquery_attention; a missing or short workspace ->
  * KF_ERR_INVALID. Device errors: KF_DEVERR_BLOCK_ID; KF_DEVERR_CONTEXT_LEN (a
- * length out of range; query ranges outside q: that request is left out); KF_DEVERR_MAX_CONTEXT (lengths above the host bounds:
- * what lies above them is left out).
+ * length out of range; query ranges outside q: that request is left out);
+ * KF_DEVERR_MAX_CONTEXT (lengths above the host bounds: what lies above them is
+ * left out).
  */
 kf_status kf_latent_attention(const void *q, const int32_t *q_start, const void *latent_cache,
                               const int32_t *block_tables, int bt_stride,
@@ -597,7 +599,8 @@ size_t kf_latent_expanded_workspace_size(int batch, int num_q_tokens, int max_co
  *   score_stride >= max_context_len
  *
  * Host errors as kf_paged_multiquery_attention, plus score_stride <
- * max_context_len -> KF_ERR_INVALID. Device errors as kf_latent_attention.
+ * max_context_len -> KF_ERR_INVALID, max_context_len above 2^30 ->
+ * KF_ERR_UNSUPPORTED. Device errors as kf_latent_attention.
  * The _fp8 call reads an E4M3 key cache with k_scale f32 [num_kv_heads].
  */
 kf_status kf_accumulate_attention(const void *q, const int32_t *q_start, const void *k_cache,
@@ -649,7 +652,8 @@ kf_status kf_accumulate_attention_fp8(const void *q, const int32_t *q_start, con
  *
  * Host errors: null pointers, sizes out of range, part of the three position
  * arrays -> KF_ERR_INVALID; row_bytes not a multiple of 16 (or above 1 MiB),
- * block_size other than 16 or 32 -> KF_ERR_UNSUPPORTED. Device errors:
+ * block_size other than 16 or 32, max_context_len above 2^30 ->
+ * KF_ERR_UNSUPPORTED. Device errors:
  * KF_DEVERR_CONTEXT_LEN, KF_DEVERR_MAX_CONTEXT (tokens at and above
  * max_context_len are dropped), KF_DEVERR_BLOCK_ID (that row does not move).
  */

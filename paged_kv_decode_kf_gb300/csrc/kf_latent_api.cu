@@ -20,6 +20,9 @@ bool aligned4(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0
 bool block_ok(int bs) { return bs == 16 || bs == 32; }
 size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
 
+// Token indices, and those a tile or a block's stride further on, stay in 31 bits.
+constexpr int64_t kMaxTokens = (int64_t)1 << 30;
+
 // A launch refused for its shape (a grid or tensor map that does not fit) is an
 // unsupported shape; anything else is a CUDA error.
 kf_status from_launch(cudaError_t e) {
@@ -46,7 +49,8 @@ kf_status latent_args(LatentParams *p, const void *q, const int32_t *q_start, co
         return KF_ERR_UNSUPPORTED;
     // one row index of q, and one 8-token group of the cache, fit the 31-bit TMA coordinates
     if (batch > 65535 || num_heads > 1024 || (int64_t)num_q_tokens * num_heads > 0x7fffffff ||
-        num_blocks * (block_size / 8) > 0x7fffffff || (int64_t)bt_stride * block_size > 0x7fffffff)
+        num_blocks * (block_size / 8) > 0x7fffffff || (int64_t)bt_stride * block_size > 0x7fffffff ||
+        std::min<int64_t>(max_context_len, (int64_t)bt_stride * block_size) > kMaxTokens)
         return KF_ERR_UNSUPPORTED;
     p->q = static_cast<const uint16_t *>(q);
     p->q_start = q_start;
@@ -94,7 +98,7 @@ kf_status accumulate_impl(const void *q, const int32_t *q_start, const void *k_c
         return KF_ERR_UNSUPPORTED;
     // q's rows and the cache's 8-token groups fit 31 bits (TMA coordinates, column counts)
     if (batch > 65535 || (int64_t)num_q_tokens * num_q_heads > 0x7fffffff ||
-        num_blocks * (block_size / 8) > 0x7fffffff)
+        num_blocks * (block_size / 8) > 0x7fffffff || max_context_len > kMaxTokens)
         return KF_ERR_UNSUPPORTED;
     AccumulateParams p;
     int sms = 0;
@@ -265,7 +269,8 @@ kf_status kf_evict_tokens(void *cache_a, void *cache_b, int64_t row_bytes, const
         !aligned4(scores_out) || !aligned4(positions) || !aligned4(positions_out) || !aligned4(seq_lens) ||
         !aligned4(context_lens) || !aligned4(context_lens_out) || !aligned4(block_tables))
         return KF_ERR_INVALID;
-    if (row_bytes % 16 != 0 || row_bytes > (1 << 20) || !block_ok(block_size) || batch > 65535)
+    if (row_bytes % 16 != 0 || row_bytes > (1 << 20) || !block_ok(block_size) || batch > 65535 ||
+        max_context_len > kMaxTokens)
         return KF_ERR_UNSUPPORTED;
     if (workspace_bytes < kf_evict_workspace_size(batch, max_context_len, keep)) return KF_ERR_INVALID;
     EvictParams p;

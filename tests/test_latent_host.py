@@ -138,6 +138,16 @@ def test_evict_host_checks(kf):
     assert kf.kf_evict_workspace_size(2, 64, 0) == 0 and kf.kf_evict_workspace_size(-1, 64, 8) == 0
 
 
+def test_token_counts_past_31_bits_are_refused(kf):
+    """A tile's or a block's stride past the last token stays inside 31 bits."""
+    lib, n = kf.raw(), (1 << 30) + 16
+    for call in (_latent, _expanded):
+        assert call(lib, mc=n, st=n // 16) == kf.KF_ERR_UNSUPPORTED
+    for fp8 in (False, True):
+        assert _acc(lib, fp8, mc=n, ss=n) == kf.KF_ERR_UNSUPPORTED
+    assert _evict(lib, mc=n, ss=n) == kf.KF_ERR_UNSUPPORTED
+
+
 def test_bindings_refuse_shapes_and_host_tensors(kf):
     bf, i32 = torch.bfloat16, torch.int32
     q = torch.zeros(2, 4, 576, dtype=bf)
