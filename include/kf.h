@@ -590,8 +590,8 @@ size_t kf_latent_expanded_workspace_size(int batch, int num_q_tokens, int max_co
  * written. q and q_start as kf_paged_multiquery_attention (q_start NULL: one
  * query token a request); lse is what the attention call over the same queries
  * returned, so that the weights are those of that call (with extra partials
- * merged, say, weights of the whole). A row whose lse is -inf adds nothing. Each
- * sum runs in one fixed order: equal calls give equal bits.
+ * merged, say, weights of the whole). A row whose lse is -inf adds nothing,
+ * whatever it holds. Each sum runs in one fixed order: equal calls give equal bits.
  *
  *   lse         f32 [num_q_tokens, num_q_heads]
  *   scores_in   f32 [batch, score_stride], or NULL for zeros

@@ -16,7 +16,7 @@
 // four lanes of a row cover 64 contiguous bytes a load. A warp holds 32 tokens of
 // one head (64 E4M3 ones; 64 registers at D = 128), twelve warps an SM some 96 KB in
 // flight, against the 45-60 KB that cover HBM's latency. Q comes through L1.
-// Measured: 64 requests of 4K tokens, 32 / 8 heads, bf16: 90 us, 5.7 TB/s of K.
+// Measured: 64 requests of 4K tokens, 32 / 8 heads, bf16: 89 us, 5.7 TB/s of K.
 // E4M3 keys widen to fp16 (exact); q goes to fp16 times a power of two that puts
 // the row's largest magnitude just below 2^15 (exact for every number within 2^-29
 // of it), undone with the key's scale.
@@ -39,8 +39,8 @@ using namespace tc;
 constexpr int kWarps = 4;  // warps a CTA
 // 16-token tiles a warp holds, and CTAs an SM: as many keys in flight either way, and
 // enough of them a warp to pay for q's conversion (64 requests of 4K, bf16: 90 us with
-// 2 tiles x 3 CTAs, 93 with 2 x 4, 96 with 1 x 6 and 4 x 2; ragged E4M3: 145 us with
-// 4 x 3, 155 with 2 x 4, 199 with 1 x 6).
+// 2 tiles x 3 CTAs, 93 with 2 x 4, 96 with 1 x 6 and 4 x 2; ragged E4M3: 146 us with
+// 4 x 3, 155 with 2 x 4, 199 with 1 x 6, and 136 once L2 fetches keys by 256 bytes).
 template <bool KV8>
 struct Held {
     static constexpr int kTiles = KV8 ? 4 : 2, kCtas = 3;
@@ -74,7 +74,8 @@ struct Columns {
     __device__ __forceinline__ void ready(float scale_log2, float kscale) {
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
-            lse2[u] = lse2[u] == -INFINITY ? INFINITY : lse2[u] * 1.4426950408889634f;
+            if (lse2[u] == -INFINITY) hide[u] = -1;  // nothing, whatever its scores are
+            lse2[u] *= 1.4426950408889634f;
             c[u] = scale_log2;
         }
         if (KV8) {
@@ -136,8 +137,8 @@ struct ColumnWalk {
         left = (int)(cols - c0);
     }
 
-    // Asks for eight columns (zeros, and no weight, past the last); Columns::ready
-    // makes them fragments. What lies between the two hides the loads.
+    // Asks for eight columns (zeros, with the lse of a row that saw nothing, past the
+    // last: zero times an infinite key is no number); Columns::ready makes them fragments. What lies between the two hides the loads.
     __device__ __forceinline__ void load(Columns<D> &x) const {
         const int lane = threadIdx.x & 31, g = lane >> 2, t4 = lane & 3;
 #pragma unroll
@@ -147,7 +148,7 @@ struct ColumnWalk {
         }
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
-            x.lse2[u] = 2 * t4 + u < left ? __ldg(lse[u]) : INFINITY;
+            x.lse2[u] = 2 * t4 + u < left ? __ldg(lse[u]) : -INFINITY;
             x.hide[u] = hide[u];
         }
     }
@@ -203,7 +204,8 @@ __device__ __forceinline__ void add_columns(const uint4 (&kr)[T][2][KV8 ? D / 64
             }
         }
     }
-    // (the newest token of a window hides from the older queries: a few runs only)
+    // (all the tokens a lane has may be hidden from a column: the newest ones from older
+    // queries, all of them from a column that adds nothing)
     if (__all_sync(0xffffffffu, t0 + 16 * T - 1 <= min(q.hide[0], q.hide[1]))) {
 #pragma unroll
         for (int k = 0; k < T; ++k)

@@ -44,6 +44,20 @@ struct AShape {
     static_assert(kSmemBytes <= 226 * 1024, "rings");
 };
 
+// Barrier `id` over 128 threads; whether `x` holds for all of them.
+__device__ __forceinline__ bool bar_all(int id, bool x) {
+    uint32_t all;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.u32 p, %1, 0;\n\t"
+        "barrier.cta.red.and.pred q, %2, 128, p;\n\t"
+        "selp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(all)
+        : "r"((uint32_t)x), "r"(id)
+        : "memory");
+    return all != 0;
+}
+
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
 accumulate_tc05_kernel(const AccumulateParams p, const __grid_constant__ CUtensorMap tmap_k,
@@ -237,17 +251,18 @@ accumulate_tc05_kernel(const AccumulateParams p, const __grid_constant__ CUtenso
                     const uint32_t sb = nq & 3, par = mine++ & 1;
                     // the columns' lse, one a thread; used by all
                     const int col = c0 + row;
-                    float l = INFINITY;
+                    float l = -INFINITY;
                     if (col < t.cols)
                         l = __ldg(p.lse + (t.r.q0 + (col >> log_g)) * p.num_q_heads + (h << log_g) +
                                   (col & ((1 << log_g) - 1)));
-                    sm_lse[half][par][row] = l == -INFINITY ? INFINITY : l * 1.4426950408889634f;  // weight 0
-                    asm volatile("barrier.cta.sync %0, 128;" ::"r"(1 + half) : "memory");
+                    sm_lse[half][par][row] = l * 1.4426950408889634f;
+                    const bool all_add = bar_all(1 + half, l != -INFINITY);
                     if (!fail) fail = !warp_wait(s_full(sb), (nq >> 2) & 1);
                     tc05::fence_after_sync();
                     const int ncol = min(kCols, t.cols - c0);
-                    // every column of the group is there and sees every token of the warp
-                    const bool fast = __all_sync(0xffffffffu, ncol == kCols && cmin <= c0);
+                    // every column of the group is there, adds something (an lse of -inf: nothing,
+                    // whatever the scores are) and sees every token of the warp
+                    const bool fast = __all_sync(0xffffffffu, all_add && cmin <= c0);
                     const float4 *lse4 = reinterpret_cast<const float4 *>(sm_lse[half][par]);
                     float2 acc = make_float2(0.f, 0.f);
                     const float2 c2 = make_float2(c, c);
@@ -272,8 +287,9 @@ accumulate_tc05_kernel(const AccumulateParams p, const __grid_constant__ CUtenso
                         } else {
 #pragma unroll
                             for (int e = 0; e < 32; ++e) {
-                                const float w = ex2f(fmaf(__uint_as_float(x[e]), c, -sm_lse[half][par][k + e]));
-                                if (k + e < ncol && c0 + k + e >= cmin) acc.x += w;
+                                const float l2 = sm_lse[half][par][k + e];  // (-inf past the last column)
+                                const float w = ex2f(fmaf(__uint_as_float(x[e]), c, -l2));
+                                if (l2 != -INFINITY && c0 + k + e >= cmin) acc.x += w;
                             }
                         }
                     }

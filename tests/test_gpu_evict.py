@@ -124,6 +124,34 @@ def test_accumulate_rows_without_weight_and_masked_nan(kf):
     _run_acc(kf, tuple(a), lens, counts, True)
 
 
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("counts", [[1, 1], [3, 40]])
+@pytest.mark.parametrize("hq,hkv", [(8, 2), (16, 2)])
+def test_accumulate_nan_queries_without_weight(kf, fp8, counts, hq, hkv):
+    """A query that holds NaN adds nothing where its lse is -inf."""
+    lens = [150, 90]
+    a = _acc_inputs(lens, counts, hq, hkv, 128, 16, fp8, seed=79)
+    a[4][0, 1] = float("nan")
+    a[5][0, 1] = -float("inf")
+    a[4][-1, hq - 1] = float("nan")
+    a[5][-1, hq - 1] = -float("inf")
+    _run_acc(kf, a, lens, counts, True)
+    _run_acc(kf, a, lens, counts, False)
+
+
+@pytest.mark.parametrize("counts", [[1, 1], [3, 2], [20, 40]])
+@pytest.mark.parametrize("hq", [2, 8, 16])
+def test_accumulate_infinite_keys(kf, counts, hq):
+    """Tokens whose scores are all -inf (an infinite number in the key) get nothing."""
+    lens = [150, 90]
+    a = _acc_inputs(lens, counts, hq, 2, 64, 16, False, seed=80)
+    a[4][..., 5] = -a[4][..., 5].abs() - 1
+    for b, t in ((0, 0), (0, 70), (0, 149), (1, 33)):
+        a[0][int(a[1][b, t // 16]), t % 16, :, 5] = float("inf")
+    _run_acc(kf, a, lens, counts, True)
+    _run_acc(kf, a, lens, counts, False)
+
+
 def test_accumulate_equal_bits_and_errors(kf):
     lens, counts = [300, 100], [1, 1]
     a = list(_acc_inputs(lens, counts, 32, 8, 128, 16, False, seed=78))
