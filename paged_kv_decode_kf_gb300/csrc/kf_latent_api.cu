@@ -62,7 +62,7 @@ kf_status latent_args(LatentParams *p, const void *q, const int32_t *q_start, co
     p->num_blocks = num_blocks;
     p->bt_stride = bt_stride;
     p->max_context_len = max_context_len;
-    p->max_query_len = max_query_len;
+    p->max_query_len = std::min(max_query_len, num_q_tokens);  // (what follows is sized by it)
     p->batch = batch;
     p->num_q_tokens = num_q_tokens;
     p->num_heads = num_heads;
@@ -116,7 +116,7 @@ kf_status accumulate_impl(const void *q, const int32_t *q_start, const void *k_c
     p.score_stride = score_stride;
     p.bt_stride = bt_stride;
     p.max_context_len = max_context_len;
-    p.max_query_len = max_query_len;
+    p.max_query_len = std::min(max_query_len, num_q_tokens);
     p.batch = batch;
     p.num_q_tokens = num_q_tokens;
     p.num_q_heads = num_q_heads;

@@ -101,12 +101,21 @@ expanded_kernel(const LatentParams p, const ExpandedKV kv, int q_tiles, const __
     }
     const int H = p.num_heads;
     const LatentRequest rq = latent_request(p, b, threadIdx.x == 0 && blockIdx.x == 0);
-    if (rq.q0 < 0) return;
+    // Every path waits for the expansion once, those with nothing to do as well: a grid that
+    // no thread waits in could end before it, and what follows in the stream begin.
+    auto expansion_done = [] { asm volatile("griddepcontrol.wait;" ::: "memory"); };
+    if (rq.q0 < 0) {
+        expansion_done();
+        return;
+    }
     const int64_t C = rq.C < p.max_query_len ? rq.C : p.max_query_len;
     const int64_t L = rq.L < p.max_context_len ? rq.L : p.max_context_len;
     const int64_t shift = rq.L - rq.C;  // query j sees tokens [0, min(shift + j + 1, L))
     const int64_t row0 = (int64_t)qg * 2 * kRows;
-    if (row0 >= C) return;
+    if (row0 >= C) {
+        expansion_done();
+        return;
+    }
     const int64_t nrows = C - row0 < 2 * kRows ? C - row0 : 2 * kRows;
     const int nqt = nrows > kRows ? 2 : 1;
     int64_t t_end = L;
@@ -118,6 +127,7 @@ expanded_kernel(const LatentParams p, const ExpandedKV kv, int q_tiles, const __
     const int64_t at = (rq.q0 + (row_ok ? row : 0)) * H + h;  // (token, head) index of this thread's row
 
     if (t_end <= 0) {
+        expansion_done();
         if (row_ok) {
             for (int i = 0; i < DV; ++i) {
                 if (p.out_dtype == KF_F32) static_cast<float *>(p.out)[at * DV + i] = 0.f;
@@ -130,7 +140,7 @@ expanded_kernel(const LatentParams p, const ExpandedKV kv, int q_tiles, const __
     const int ntiles = (int)((t_end + kTok - 1) / kTok);
     // the expansion's keys and values are complete from here on (its inputs, which this
     // kernel read above, were so before it started)
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    expansion_done();
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < NS; ++i) {

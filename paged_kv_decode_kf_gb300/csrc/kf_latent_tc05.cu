@@ -895,7 +895,6 @@ cudaError_t launch_latent(const LatentParams &p, void *workspace, int sm_count, 
     sm_count = std::max(sm_count, 2);
     CUtensorMap mx, mq;
     if (!encode_cache(fn, &mx, p) || !encode_q(fn, &mq, p)) return cudaErrorInvalidValue;
-    // no more CTAs than the batch can have tiles
     // Requests of more than one unit: two CTAs walk a run together, a unit each, so that
     // one's tiles are the other's L2 hits (64 requests of 4K tokens, 128 heads: 117 us
     // against 130, which read 550 MB from HBM for a cache of 302). With one unit a

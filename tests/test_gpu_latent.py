@@ -449,6 +449,16 @@ def test_expanded_graph(kf):
         c.check(out.cpu(), lse.cpu())
 
 
+def test_loose_host_bounds(kf):
+    """Host bounds far above the real ones cost nothing but the expanded workspace."""
+    for w in (None, 128):
+        c = Case([70, 9], [3, 2], 4, 512, seed=61, w=w)
+        c.max_q = 2 ** 31 - 1
+        if w is None:
+            c.max_ctx = 2 ** 31 - 1
+        c.check(*c.run(kf))
+
+
 def test_expanded_agrees_with_absorbed(kf):
     """One batch through both forms, projections by plain products."""
     c = Case([90, 200], [5, 20], 8, 512, 16, seed=49, w=128)
