@@ -483,3 +483,58 @@ def test_expanded_out_of_range_is_reported(kf):
     c.cache.fill_(8.0)          # 256 * 8 * 500 is far above fp16's largest number
     c.run(kf)
     assert kf.kf_get_device_error() == kf.KF_DEVERR_RANGE
+
+
+def test_calls_on_several_streams_at_once(kf):
+    """Calls that share inputs but no workspace, on four streams together, give the bits
+    that each gives alone."""
+    g = torch.Generator().manual_seed(71)
+    lens = [700, 33, 1500, 260]
+    one = Case(lens, [1] * 4, 128, 512, seed=72)
+    q1, cache, table, ctx, qs1 = one.dev()
+    many = Case(lens, [200, 33, 300, 7], 4, 512, seed=72, w=128)
+    q2, cache2, table2, ctx2, qs2 = many.dev()
+    uk, uv = many.w_uk.cuda(), many.w_uv.cuda()
+    q3 = torch.randn(4 * 24, 16, 128, generator=g).to(torch.bfloat16).cuda()
+    qs3 = torch.arange(0, 4 * 24 + 1, 24, dtype=torch.int32).cuda()
+    k = torch.randn(int(table.max()) + 1, 16, 2, 128, generator=g).to(torch.bfloat16).cuda()
+    lse3 = torch.full((4 * 24, 16), 6.0, device="cuda")
+    scores = torch.rand(4, 1500, generator=g).cuda()
+    rows = torch.randint(0, 255, (int(table.max()) + 1, 16, 2048), generator=g, dtype=torch.uint8).cuda()
+    kept = torch.empty(4, dtype=torch.int32, device="cuda")
+    outs = {n: t.cuda() for n, t in (
+        ("absorbed", torch.zeros(4, 128, 512)), ("absorbed lse", torch.zeros(4, 128)),
+        ("expanded", torch.zeros(q2.shape[0], 4, 128)), ("expanded lse", torch.zeros(q2.shape[0], 4)),
+        ("weights", torch.zeros(4, 1500)), ("kept scores", torch.zeros(4, 1500)))}
+    w1 = kf.make_latent_workspace(4, 1, 128, 512)
+    w2 = kf.make_latent_expanded_workspace(4, q2.shape[0], 1500, 4, 128, 128)
+    w4 = kf.make_evict_workspace(4, 1500, 250)
+    calls = (
+        lambda: kf.kf_latent_attention(q1, cache, table, ctx, 1500, one.scale, w1, out=outs["absorbed"],
+                                       lse_out=outs["absorbed lse"]),
+        lambda: kf.kf_latent_attention_expanded(q2, cache2, uk, uv, table2, ctx2, 1500, many.scale, w2, q_start=qs2,
+                                                max_query_len=300, out=outs["expanded"],
+                                                lse_out=outs["expanded lse"]),
+        lambda: kf.kf_accumulate_attention(q3, k, table, ctx, 1500, 128 ** -0.5, lse3, outs["weights"], q_start=qs3,
+                                           max_query_len=24),
+        # (no source is a destination: the same call again moves the same rows)
+        lambda: kf.kf_evict_tokens([rows], table, ctx, 1500, scores, 250, 4, 32, kept, outs["kept scores"], w4),
+    )
+    for call in calls:
+        call()
+    torch.cuda.synchronize()
+    alone = {n: t.clone() for n, t in outs.items()}
+    rows_alone = rows.clone()
+    streams = [torch.cuda.Stream() for _ in calls]
+    for _ in range(5):
+        for t in outs.values():
+            t.zero_()
+        torch.cuda.synchronize()
+        for _ in range(4):
+            for s, call in zip(streams, calls):
+                with torch.cuda.stream(s):
+                    call()
+        torch.cuda.synchronize()
+        for n, t in outs.items():
+            assert torch.equal(t, alone[n]), n
+        assert torch.equal(rows, rows_alone)
