@@ -486,10 +486,6 @@ def _on(index: int, t: torch.Tensor, dtype, name: str) -> int:
     return _dev(t, dtype, name)   # names what is wrong
 
 
-def _opt(index: int, t: Optional[torch.Tensor], dtype, name: str) -> Optional[int]:
-    return None if t is None else _on(index, t, dtype, name)
-
-
 KF_ROPE_DIM = 64  # width of the rotary part of a latent row
 
 
@@ -694,35 +690,40 @@ def kf_evict_tokens(caches, block_tables: torch.Tensor, context_lens: torch.Tens
                     scores_out: torch.Tensor, workspace: torch.Tensor, positions: Optional[torch.Tensor] = None,
                     seq_lens: Optional[torch.Tensor] = None, positions_out: Optional[torch.Tensor] = None,
                     stream=None) -> None:
-    """Cut every request to its `keep` tokens of most weight, in place. caches: one
-    or two paged caches ([num_blocks, block_size, ...], rows of equal bytes: K and
+    """Cut every request to its `keep` tokens of most weight, in place. caches: a
+    list of one or two paged caches ([num_blocks, block_size, ...], rows of equal bytes: K and
     V, or a latent cache). The *_out tensors may be their inputs."""
-    caches = list(caches)
-    if len(caches) not in (1, 2):
+    if isinstance(caches, torch.Tensor) or len(caches) not in (1, 2):
         raise ValueError("caches must be one or two tensors")
     first = caches[0]
-    for c in caches:
-        if c.dim() < 3 or c.shape != first.shape or c.dtype != first.dtype:
-            raise ValueError("caches must share one [num_blocks, block_size, ...] shape and type")
+    shape = first.shape
+    if len(shape) < 3 or (len(caches) == 2 and (caches[1].shape != shape or caches[1].dtype != first.dtype)):
+        raise ValueError("caches must share one [num_blocks, block_size, ...] shape and type")
     dev = first.get_device()
-    nb, bs = first.shape[:2]
-    row_bytes = first.stride(1) * first.element_size()
-    B = block_tables.shape[0]
-    for t, n in ((context_lens, "context_lens"), (context_lens_out, "context_lens_out"), (seq_lens, "seq_lens")):
-        if t is not None:
-            _shape(t, (B,), n)
-    if scores.dim() != 2 or scores.shape[0] != B:
+    cache_a = _on(dev, first, first.dtype, "caches")
+    cache_b = _on(dev, caches[1], first.dtype, "caches") if len(caches) == 2 else None
+    B, columns = block_tables.shape
+    _shape(context_lens, (B,), "context_lens")
+    _shape(context_lens_out, (B,), "context_lens_out")
+    width = scores.shape
+    if len(width) != 2 or width[0] != B:
         raise ValueError("scores must be [batch, stride]")
-    for t, n in ((scores_out, "scores_out"), (positions, "positions"), (positions_out, "positions_out")):
-        if t is not None:
-            _shape(t, scores.shape, n)
-    ptr = [_on(dev, c, c.dtype, "caches") for c in caches] + [None]
+    _shape(scores_out, width, "scores_out")
+    pos = pos_out = seq = None
+    if positions is not None:
+        _shape(positions, width, "positions")
+        pos = _on(dev, positions, torch.int32, "positions")
+    if positions_out is not None:
+        _shape(positions_out, width, "positions_out")
+        pos_out = _on(dev, positions_out, torch.int32, "positions_out")
+    if seq_lens is not None:
+        _shape(seq_lens, (B,), "seq_lens")
+        seq = _on(dev, seq_lens, torch.int32, "seq_lens")
     _call("kf_evict_tokens", dev, stream,
-          ptr[0], ptr[1], row_bytes, _on(dev, block_tables, torch.int32, "block_tables"), block_tables.shape[1],
-          _on(dev, context_lens, torch.int32, "context_lens"), int(max_context_len), B, bs, nb,
-          _on(dev, scores, torch.float32, "scores"), _on(dev, scores_out, torch.float32, "scores_out"), scores.shape[1],
-          _opt(dev, positions, torch.int32, "positions"), _opt(dev, positions_out, torch.int32, "positions_out"),
-          _opt(dev, seq_lens, torch.int32, "seq_lens"), int(keep), int(sink), int(recent),
+          cache_a, cache_b, first.stride(1) * first.element_size(), _on(dev, block_tables, torch.int32, "block_tables"),
+          columns, _on(dev, context_lens, torch.int32, "context_lens"), int(max_context_len), B, shape[1], shape[0],
+          _on(dev, scores, torch.float32, "scores"), _on(dev, scores_out, torch.float32, "scores_out"), width[1],
+          pos, pos_out, seq, int(keep), int(sink), int(recent),
           _on(dev, context_lens_out, torch.int32, "context_lens_out"), _on(dev, workspace, torch.uint8, "workspace"),
           workspace.numel())
 

@@ -175,3 +175,14 @@ def test_bindings_refuse_shapes_and_host_tensors(kf):
     with pytest.raises(ValueError, match="positions"):
         kf.kf_evict_tokens([k], bt, ctx, 16, torch.zeros(2, 16), 4, 0, 0, ctx, torch.zeros(2, 16), ws,
                            positions=torch.zeros(2, 15, dtype=i32))
+
+
+def test_evict_refuses_caches_that_are_no_list(kf):
+    i32 = torch.int32
+    kv, ctx, sc = torch.zeros(2, 16, 2, 64), torch.ones(2, dtype=i32), torch.zeros(2, 32)
+    args = (torch.zeros(2, 2, dtype=i32), ctx, 32, sc, 8, 0, 0, ctx, sc, torch.zeros(64, dtype=torch.uint8))
+    for caches in (kv, [], [kv, kv, kv]):
+        with pytest.raises(ValueError, match="one or two"):
+            kf.kf_evict_tokens(caches, *args)
+    with pytest.raises(ValueError, match="share one"):
+        kf.kf_evict_tokens([kv, kv[:1]], *args)
