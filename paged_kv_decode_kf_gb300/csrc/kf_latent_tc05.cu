@@ -61,20 +61,22 @@ using namespace mq5;
 
 // Rows a unit: O^T takes R / 128 * (rows a unit) of TMEM's columns, 256 either way.
 __host__ __device__ constexpr int unit_rows(int latent_dim) { return latent_dim == 512 ? 64 : 128; }
-constexpr int kN = 64;   // tokens a tile
-constexpr int kAhead = 2;  // tiles fetched into L2 ahead of the ring's loads
+// Tokens a tile.
+__host__ __device__ constexpr int tile_tokens(int latent_dim) { return latent_dim == 512 ? 32 : 64; }
+constexpr int kAhead = 1;  // tiles fetched into L2 ahead of the ring's loads
 constexpr int kSoftThreads = 128, kProducerWarp = 4, kScoreWarp = 5, kValueWarp = 6, kThreads = 224;
 
 template <int R>
 struct LShape {
-    static constexpr int kM = unit_rows(R);
+    static constexpr int kM = unit_rows(R), kN = tile_tokens(R);
     static constexpr int kAtoms = (R + kRopeDim) / 64;
     static constexpr int kGroupBytes = kAtoms * 1024;         // 8 tokens
     static constexpr int kTileBytes = kN / 8 * kGroupBytes;
     static constexpr int kQAtomBytes = kM * 128;              // the rows x 64 columns
     static constexpr int kQBytes = kAtoms * kQAtomBytes;
-    static constexpr int kPBytes = kM * kN * 2;
-    static constexpr int kStages = R == 512 ? 2 : 3;
+    static constexpr int kPBytes = kM * 128;
+    static constexpr int kPBuffers = 64 / kN;  // weights of a tile: a row's 128 bytes hold 64 tokens
+    static constexpr int kStages = R == 512 ? 4 : 3;
     static constexpr int kSmemBytes = kQBytes + kStages * kTileBytes + kPBytes + 1024;
     static constexpr int kDimTiles = R / 128;
     static constexpr uint32_t kColS = 256;                    // two score tiles; O^T below
@@ -100,6 +102,7 @@ __device__ __forceinline__ Request request_of(const LatentParams &p, int b, bool
     q.rows = C * p.num_heads;
     q.L = r.L < p.max_context_len ? r.L : p.max_context_len;
     q.shift = r.L - r.C;
+    const int kN = tile_tokens(p.latent_dim);
     q.n = q.L > 0 ? (q.L + kN - 1) / kN : 1;
     const int M = unit_rows(p.latent_dim);
     q.units = (int)((q.rows + M - 1) / M);
@@ -172,6 +175,7 @@ struct Walker {
                 if (lim < end) end = lim < 0 ? 0 : lim;
             }
             s.t_end = (int)end;
+            const int kN = tile_tokens(p.latent_dim);
             const int64_t valid = (end + kN - 1) / kN;  // tiles any row sees
             const int64_t hi = tile + len < valid ? tile + len : valid;
             s.tile0 = (int)tile;
@@ -203,19 +207,16 @@ struct Partials {
 // ---------------------------------------------------------------------------
 // PTX
 // ---------------------------------------------------------------------------
-// 16 lanes x 64 columns: lane l gets columns 8 i + 2 (l % 4) + {0, 1} of TMEM lanes
+// 16 lanes x 32 columns: lane l gets columns 8 i + 2 (l % 4) + {0, 1} of TMEM lanes
 // l / 4 (r[4 i], r[4 i + 1]) and l / 4 + 8 (r[4 i + 2], r[4 i + 3]), waited for.
-__device__ __forceinline__ void tmem_ld_16x256b_x8(uint32_t taddr, uint32_t (&r)[32]) {
+__device__ __forceinline__ void tmem_ld_16x256b_x4(uint32_t taddr, uint32_t (&r)[16]) {
     asm volatile(
-        "tcgen05.ld.sync.aligned.16x256b.x8.b32 {"
-        "%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
-        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31"
-        "}, [%32];\n\t"
+        "tcgen05.ld.sync.aligned.16x256b.x4.b32 {"
+        "%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15"
+        "}, [%16];\n\t"
         "tcgen05.wait::ld.sync.aligned;"
         : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
-          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
-          "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
-          "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
         : "r"(taddr)
         : "memory");
 }
@@ -292,9 +293,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 latent_kernel(const LatentParams p, const Partials part, int twins, const __grid_constant__ CUtensorMap tmap_x,
               const __grid_constant__ CUtensorMap tmap_q) {
     using Sh = LShape<R>;
-    constexpr int NS = Sh::kStages, KS = (R + kRopeDim) / 16, KP = kN / 16, kM = Sh::kM;
-    // full[NS], empty[NS], q_full, q_empty, s_full[2], s_empty[2], p_full, pv_done, o_empty, fin[2]
-    __shared__ __align__(8) uint64_t bar_mem[2 * NS + 11];
+    constexpr int NS = Sh::kStages, NP = Sh::kPBuffers, KS = (R + kRopeDim) / 16, kN = Sh::kN, KP = kN / 16, kM = Sh::kM;
+    // full[NS], empty[NS], q_full, q_empty, s_full[2], s_empty[2], p_full[2], pv_done[2], o_empty, fin[2]
+    __shared__ __align__(8) uint64_t bar_mem[2 * NS + 13];
     __shared__ int64_t sm_loc[36];
     __shared__ float sm_alpha[kM], sm_lse[kM];
     __shared__ uint32_t tmem_slot;
@@ -308,7 +309,9 @@ latent_kernel(const LatentParams p, const Partials part, int twins, const __grid
     const uint32_t q_full = bars + 8u * (2 * NS), q_empty = q_full + 8;
     auto s_full = [&](uint32_t i) { return q_full + 16 + 8 * i; };
     auto s_empty = [&](uint32_t i) { return q_full + 32 + 8 * i; };
-    const uint32_t p_full = q_full + 48, pv_done = q_full + 56, o_empty = q_full + 64, fin = q_full + 72;
+    auto p_full = [&](uint32_t i) { return q_full + 48 + 8 * (i % NP); };   // of tile i
+    auto pv_done = [&](uint32_t i) { return q_full + 64 + 8 * (i % NP); };
+    const uint32_t o_empty = q_full + 80, fin = q_full + 88;
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
 
     if (threadIdx.x == 0) {
@@ -319,8 +322,10 @@ latent_kernel(const LatentParams p, const Partials part, int twins, const __grid
             mbar_init(s_full(i), 1);
             mbar_init(s_empty(i), kSoftThreads);
         }
-        mbar_init(p_full, kSoftThreads);
-        mbar_init(pv_done, 1);
+        for (int i = 0; i < NP; ++i) {
+            mbar_init(p_full(i), kSoftThreads);
+            mbar_init(pv_done(i), 1);
+        }
         mbar_init(o_empty, kSoftThreads);
         mbar_init(fin, 1);
         mbar_init(fin + 8, 1);
@@ -480,7 +485,7 @@ latent_kernel(const LatentParams p, const Partials part, int twins, const __grid
             ok = warp_wait(o_empty, (nseg & 1) ^ 1);
             for (int i = 0; i < tiles && ok; ++i, ++g) {
                 const uint32_t st = g % NS;
-                ok = !__any_sync(0xffffffffu, abort_flag) && warp_wait(p_full, g & 1);
+                ok = !__any_sync(0xffffffffu, abort_flag) && warp_wait(p_full(g), (g / NP) & 1);
                 if (!ok) break;
                 tc05::fence_after_sync();
                 const uint64_t cd = tc05::sdesc_sw128(sX + st * Sh::kTileBytes, 1024, Sh::kGroupBytes);
@@ -491,9 +496,9 @@ latent_kernel(const LatentParams p, const Partials part, int twins, const __grid
 #pragma unroll
                         for (int kk = 0; kk < KP; ++kk)
                             tc05::mma_ss(tm + kM * d, cd + (uint64_t)((d * 2048 + kk * 2 * Sh::kGroupBytes) / 16),
-                                         pd + (uint64_t)(32 * kk / 16), id_o, (i > 0 || kk > 0) ? 1u : 0u);
+                                         pd + (uint64_t)(((g % NP) * kN * 2 + 32 * kk) / 16), id_o, (i > 0 || kk > 0) ? 1u : 0u);
                     tc05::commit(empty(st));
-                    tc05::commit(pv_done);
+                    tc05::commit(pv_done(g));
                 }
                 __syncwarp();
             }
@@ -506,7 +511,7 @@ latent_kernel(const LatentParams p, const Partials part, int twins, const __grid
         const float c = p.scale_log2;
         // This lane's rows and how their scores lie: 64 rows a unit, two rows, a quarter of
         // each; 128 rows, one whole row.
-        constexpr int NR = kM == 64 ? 2 : 1, NX = 64 / (kM == 64 ? 4 : 1);
+        constexpr int NR = kM == 64 ? 2 : 1, NX = kN / (kM == 64 ? 4 : 1);
         const int rr[2] = {kM == 64 ? 16 * warp + (lane >> 2) : (int)threadIdx.x, 16 * warp + (lane >> 2) + 8};
         auto token_of = [&](int e) { return kM == 64 ? 8 * (e >> 1) + 2 * (lane & 3) + (e & 1) : e; };
         uint32_t g = 0;
@@ -532,10 +537,10 @@ latent_kernel(const LatentParams p, const Partials part, int twins, const __grid
                 tc05::fence_after_sync();
                 float x[NR][NX];  // element e of row k: token token_of(e) of the tile
                 if (kM == 64) {
-                    uint32_t u[32];
-                    tmem_ld_16x256b_x8(tm + lane_base + Sh::kColS + 64 * sb, u);
+                    uint32_t u[16];
+                    tmem_ld_16x256b_x4(tm + lane_base + Sh::kColS + 64 * sb, u);
 #pragma unroll
-                    for (int e = 0; e < 32; ++e)  // (NR - 1 and NX - 1 are 1 and 15 here)
+                    for (int e = 0; e < 16; ++e)  // (NR - 1 and NX - 1 are 1 and 7 here)
                         x[(e >> 1) & (NR - 1)][(((e >> 2) << 1) | (e & 1)) & (NX - 1)] = __uint_as_float(u[e]);
                 } else {
                     uint32_t u[64];
@@ -604,9 +609,10 @@ latent_kernel(const LatentParams p, const Partials part, int twins, const __grid
                 // one barrier a tile in the common case; O^T is rescaled (and a wait that
                 // gave up acted on) by all four warps together
                 const bool any = soft_any(need || fail);
-                // the P buffer is free, and O^T complete, once the previous value product is done
-                // (which overlaps with the maximum above)
-                if (g > 0 && !warp_wait(pv_done, (g - 1) & 1)) fail = true;
+                // O^T is complete once the previous value product is done (the P buffer is free
+                // with the last one that read it)
+                if (any && g > 0 && !warp_wait(pv_done(g - 1), ((g - 1) / NP) & 1)) fail = true;
+                if (g >= NP && !warp_wait(pv_done(g - NP), ((g / NP) - 1) & 1)) fail = true;
                 if (any) {
                     stop = soft_any(fail);
                     if (stop) break;
@@ -645,7 +651,7 @@ latent_kernel(const LatentParams p, const Partials part, int twins, const __grid
                     if (kM == 64) {
 #pragma unroll
                         for (int e = 0; e < NX / 2; ++e)
-                            asm volatile("st.shared.u32 [%0], %1;" ::"r"(row + ((e ^ (rr[k] & 7)) << 4) + (lane & 3) * 4),
+                            asm volatile("st.shared.u32 [%0], %1;" ::"r"(row + (((e + (g % NP) * (kN / 8)) ^ (rr[k] & 7)) << 4) + (lane & 3) * 4),
                                          "r"(w[e])
                                          : "memory");
                     } else {
@@ -659,7 +665,7 @@ latent_kernel(const LatentParams p, const Partials part, int twins, const __grid
                 }
                 fence_proxy_async_smem();
                 tc05::fence_before_sync();
-                mbar_arrive(p_full);
+                mbar_arrive(p_full(g));
             }
             if (stop) break;
             // epilogue: row sums (over the lanes of a row), then O^T column by column
@@ -675,7 +681,7 @@ latent_kernel(const LatentParams p, const Partials part, int twins, const __grid
                     sm_lse[rr[k]] = l[k] != 0.f ? (m[k] + log2f(l[k])) * 0.6931471805599453f : -INFINITY;
                 }
             }
-            if (s.tiles > 0 && !warp_wait(pv_done, (g - 1) & 1)) fail = true;
+            if (s.tiles > 0 && !warp_wait(pv_done(g - 1), ((g - 1) / NP) & 1)) fail = true;
             stop = soft_any(fail);
             if (stop) break;
             const int64_t slot = 2 * (int64_t)blockIdx.x + (s.first ? 0 : 1);
@@ -904,8 +910,8 @@ cudaError_t launch_latent(const LatentParams &p, void *workspace, int sm_count, 
     const int twins = rows_max > M ? 2 : 1;
     // no more runs than the batch can have tiles
     const int64_t groups = (int64_t)p.batch * ((rows_max + twins * M - 1) / (twins * M));
-    const int64_t tiles = groups * std::max<int64_t>(1, ((int64_t)p.max_context_len + kN - 1) / kN);
-    const int ctas = twins * (int)std::min<int64_t>(std::max(1, sm_count / twins), tiles);
+    const int64_t pieces = groups * std::max<int64_t>(1, ((int64_t)p.max_context_len + 63) / 64);
+    const int ctas = twins * (int)std::min<int64_t>(std::max(1, sm_count / twins), pieces);
     Partials part;
     part.pitch = (int)row_pitch(p.max_query_len, p.num_heads, p.latent_dim);
     part.o = static_cast<float *>(workspace);
