@@ -7,8 +7,8 @@
 // so one tile of X in shared memory serves both products: keys as they are, values
 // as the same bytes read along the other axis.
 //
-// Work. Rows come in tiles of 64 (R = 512) or 128 (R = 256), tokens in tiles of 64. A
-// unit is one row tile of one request over all its token tiles; the units of the
+// Work. Rows come in tiles of 64 (R = 512) or 128 (R = 256), tokens in tiles of 32 or
+// 64. A unit is one row tile of one request over all its token tiles; the units of the
 // batch, laid end to end, are cut into equal runs, one a CTA (one CTA an SM: the
 // tile ring fills its shared memory); where requests have several units, one a pair
 // of CTAs, which walk it side by side. A run may start and end inside a unit; the parts of such a unit
@@ -16,9 +16,9 @@
 // them. So a batch of any length mix keeps every SM busy to the end, at the
 // price of at most two partials a CTA.
 //
-// One tile: 64 x (R + 64) bf16 arrive as four TMA boxes of 16 tokens, landing as
+// One tile: 32 or 64 rows of R + 64 bf16 arrive as TMA boxes of 16 tokens, landing as
 // 8-token groups of 128-byte-swizzled atoms (group, 64-column atom, token, column).
-//   S[rows x 64 tokens]        = Q X^T          A = Q, B = X, both K-major, M = the row tile
+//   S[rows x tokens]           = Q X^T          A = Q, B = X, both K-major, M = the row tile
 //   O^T[128 columns x rows]   += C^T P^T        A = C^T (M-major: the same tile), B = P
 // The value product is taken transposed, R / 128 instructions of M = 128 and N = the
 // rows in use (rounded up to 16): its accumulator then takes 256 TMEM columns instead
@@ -35,13 +35,18 @@
 // product of tile g as soon as its weights are there, whichever comes first.
 //
 // What bounds it: 2 (R + 64) bytes of cache a token. At R = 512 an SM's share of HBM
-// brings a tile of 64 tokens in 3400 cycles (73.7 KB at 44.6 B/ns); its instructions
-// take 2070 (36 S instructions of 36 cycles, 16 O^T ones of 48) and shared memory 2500
-// (fill, Q and X for S, C and P for O), so up to 64 rows the cache is the bound: 16
-// requests of 8K-256K tokens and 32 heads run at 3340 cycles a tile (200 us, 0.81 of
-// the copy bandwidth with start, epilogues and merge). With more rows the two-slot
-// ring's latency is: load (1650) + S (1300-1800) + softmax (1100) + O^T (800-1050)
-// + hand-offs, over two slots.
+// brings 64 tokens in 3400 cycles (73.7 KB at 44.6 B/ns). The instructions' operands
+// come from shared memory at 128 bytes a cycle: per 32 tokens 36 S instructions of 24
+// cycles (3 KB) and 8 O^T ones of 48 (6 KB), 2500 cycles for 64 tokens. So the cache is
+// the bound up to 64 rows: 16 requests of 8K-256K tokens and 32 heads take 185 us, 0.88
+// of the copy bandwidth with start, epilogues and merge. With more rows what bounds is
+// the chain load (1650 cycles for 64 tokens) - S - softmax - O^T over a ring that Q
+// (72 KB) leaves 144 KB for: 64 requests of 4K tokens, 128 heads: 110 us. Four slots of
+// 32 tokens cost a fifth more operand reads than two of 64 and shorten the chain: 201
+// and 116 us with two. The weights of 32 tokens are half of a swizzled 128-byte row,
+// so that two tiles' weights fit where 64 tokens' lay, and the softmax of one tile
+// writes while the value product of the last reads. More than two score tiles in TMEM
+// gain nothing.
 //
 // Tokens past a unit's last visible one are masked by selection (never multiplied)
 // and their rows zeroed in shared memory (0 * NaN would poison the product).
@@ -61,9 +66,11 @@ using namespace mq5;
 
 // Rows a unit: O^T takes R / 128 * (rows a unit) of TMEM's columns, 256 either way.
 __host__ __device__ constexpr int unit_rows(int latent_dim) { return latent_dim == 512 ? 64 : 128; }
-// Tokens a tile.
+// Tokens a tile: half as many where a token's row is twice as long.
 __host__ __device__ constexpr int tile_tokens(int latent_dim) { return latent_dim == 512 ? 32 : 64; }
-constexpr int kAhead = 1;  // tiles fetched into L2 ahead of the ring's loads
+// Tiles fetched into L2 ahead of the ring's loads (16 requests of 8K-256K tokens, 32 heads: 185 us
+// with one, 186 with two, 189 with three; 48 of 4K, R = 256: 49 / 50 / 51).
+constexpr int kAhead = 1;
 constexpr int kSoftThreads = 128, kProducerWarp = 4, kScoreWarp = 5, kValueWarp = 6, kThreads = 224;
 
 template <int R>
@@ -374,7 +381,7 @@ latent_kernel(const LatentParams p, const Partials part, int twins, const __grid
         uint32_t g = 0, nseg = 0, q_loads = 0;
         bool ok = true;
         Segment s{};
-        // lane e < 4: the cache row group of the tile's e-th 16 tokens, asked for long
+        // lane e: the cache row group of the tile's e-th 16 tokens, asked for long
         // before the tile's turn; past the last token any valid one
         auto group_of = [&](int tile) -> int {
             const int t = tile * kN + 16 * lane;
@@ -902,13 +909,14 @@ cudaError_t launch_latent(const LatentParams &p, void *workspace, int sm_count, 
     CUtensorMap mx, mq;
     if (!encode_cache(fn, &mx, p) || !encode_q(fn, &mq, p)) return cudaErrorInvalidValue;
     // Requests of more than one unit: two CTAs walk a run together, a unit each, so that
-    // one's tiles are the other's L2 hits (64 requests of 4K tokens, 128 heads: 117 us
-    // against 130, which read 550 MB from HBM for a cache of 302). With one unit a
+    // one's tiles are the other's L2 hits (64 requests of 4K tokens, 128 heads: 110 us
+    // against 119, which read 550 MB from HBM for a cache of 302). With one unit a
     // request there is nothing to share.
     const int M = unit_rows(p.latent_dim);
     const int64_t rows_max = (int64_t)p.max_query_len * p.num_heads;
     const int twins = rows_max > M ? 2 : 1;
-    // no more runs than the batch can have tiles
+    // no more runs than the batch can have pieces of 64 tokens (1 request of 777 tokens, 16 heads:
+    // 16.7 us with 13 runs, 18.6 with 25 of 32 tokens)
     const int64_t groups = (int64_t)p.batch * ((rows_max + twins * M - 1) / (twins * M));
     const int64_t pieces = groups * std::max<int64_t>(1, ((int64_t)p.max_context_len + 63) / 64);
     const int ctas = twins * (int)std::min<int64_t>(std::max(1, sm_count / twins), pieces);
@@ -921,7 +929,7 @@ cudaError_t launch_latent(const LatentParams &p, void *workspace, int sm_count, 
     part.cuts = reinterpret_cast<Cut *>(ws + al256(rows * 4));
     // few units are cut over many CTAs each: one row a merge block, its warps share
     // the partials; many units have two or three partials: one warp a row (1 request of
-    // 30K tokens, 16 heads: 31 us against 77; 32 requests of 8K: 80 against 77)
+    // 30K tokens, 16 heads: 31 us against 76; 32 requests of 8K: 73 against 70)
     const bool long_units = groups * twins * 8 < ctas;
     return p.latent_dim == 512 ? launch<512>(p, part, ctas, twins, long_units, stream, mx, mq)
                                : launch<256>(p, part, ctas, twins, long_units, stream, mx, mq);
