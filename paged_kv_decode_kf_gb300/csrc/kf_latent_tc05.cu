@@ -304,7 +304,9 @@ latent_kernel(const LatentParams p, const Partials part, int twins, const __grid
     // full[NS], empty[NS], q_full, q_empty, s_full[2], s_empty[2], p_full[2], pv_done[2], o_empty, fin[2]
     __shared__ __align__(8) uint64_t bar_mem[2 * NS + 13];
     __shared__ int64_t sm_loc[36];
-    __shared__ float sm_alpha[kM], sm_lse[kM];
+    // (1 / sum has an array of its own: a warp that still rescales O^T after the unit's last
+    // tile reads every row's alpha, and no barrier lies between that and the epilogue's sums)
+    __shared__ float sm_alpha[kM], sm_inv[kM], sm_lse[kM];
     __shared__ uint32_t tmem_slot;
     __shared__ volatile int abort_flag;
     extern __shared__ uint8_t smem_raw[];
@@ -684,7 +686,7 @@ latent_kernel(const LatentParams p, const Partials part, int twins, const __grid
                 }
                 if (kM == 128 || (lane & 3) == 0) {
                     // (no token seen: 0 and -inf; a NaN stays one)
-                    sm_alpha[rr[k]] = l[k] != 0.f ? 1.f / l[k] : 0.f;
+                    sm_inv[rr[k]] = l[k] != 0.f ? 1.f / l[k] : 0.f;
                     sm_lse[rr[k]] = l[k] != 0.f ? (m[k] + log2f(l[k])) * 0.6931471805599453f : -INFINITY;
                 }
             }
@@ -702,13 +704,13 @@ latent_kernel(const LatentParams p, const Partials part, int twins, const __grid
             // O^T: thread = column, one row a TMEM column; 32 consecutive numbers a warp and store
             if (!s.whole) {
                 float *dst = part.o + slot * part.pitch * R + threadIdx.x;
-                store_rows<R>(tm + lane_base, s.tiles > 0, s.rows, sm_alpha, [=](int r, int d, float v) { dst[r * R + d] = v; });
+                store_rows<R>(tm + lane_base, s.tiles > 0, s.rows, sm_inv, [=](int r, int d, float v) { dst[r * R + d] = v; });
             } else if (p.out_dtype == KF_F32) {
                 float *dst = static_cast<float *>(p.out) + row_out * R + threadIdx.x;
-                store_rows<R>(tm + lane_base, s.tiles > 0, s.rows, sm_alpha, [=](int r, int d, float v) { dst[r * R + d] = v; });
+                store_rows<R>(tm + lane_base, s.tiles > 0, s.rows, sm_inv, [=](int r, int d, float v) { dst[r * R + d] = v; });
             } else {
                 __nv_bfloat16 *dst = static_cast<__nv_bfloat16 *>(p.out) + row_out * R + threadIdx.x;
-                store_rows<R>(tm + lane_base, s.tiles > 0, s.rows, sm_alpha,
+                store_rows<R>(tm + lane_base, s.tiles > 0, s.rows, sm_inv,
                               [=](int r, int d, float v) { dst[r * R + d] = __float2bfloat16(v); });
             }
             if (threadIdx.x < s.rows) {
@@ -717,7 +719,7 @@ latent_kernel(const LatentParams p, const Partials part, int twins, const __grid
             }
             tc05::fence_before_sync();
             if (s.tiles > 0) mbar_arrive(o_empty);
-            soft_sync();  // sm_alpha and sm_lse are free again
+            soft_sync();  // sm_inv and sm_lse are free again
         }
         if (threadIdx.x == 0) {
             if (stop) cut.parts = 0;
