@@ -344,9 +344,11 @@ latent_kernel(const LatentParams p, const Partials part, int twins, const __grid
         asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tmap_x)) : "memory");
         asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tmap_q)) : "memory");
     }
-    if (warp == kScoreWarp) tc05::tmem_alloc(smem_u32(&tmem_slot), 512);
     // what ran before on the stream (an append, say) is complete from here on
     asm volatile("griddepcontrol.wait;" ::: "memory");
+    // (TMEM is taken after the wait: a predecessor that still has to allocate its own would
+    // wait for this kernel, and this one for it)
+    if (warp == kScoreWarp) tc05::tmem_alloc(smem_u32(&tmem_slot), 512);
     if (threadIdx.x == 0) abort_flag = (*(volatile unsigned int *)p.err & KF_DEVERR_TIMEOUT) ? 1 : 0;
     const int run = blockIdx.x / twins, runs = gridDim.x / twins;
     Walker walk;
