@@ -490,7 +490,8 @@ kf_status kf_decode_step_static(const void *q, const void *k_new, const void *v_
  *   context_lens_before  int32 [batch], tokens cached before this call (not modified)
  *
  * Device errors as kf_append_kv, a row at a time; row_start that does not
- * ascend -> KF_DEVERR_CONTEXT_LEN (those rows are not written).
+ * ascend, or that leaves [0, num_rows] -> KF_DEVERR_CONTEXT_LEN (a row is then
+ * written once, at its place for a request whose range holds it, or not at all).
  */
 kf_status kf_append_latent(const void *latent_new, const int32_t *row_start, void *latent_cache,
                            const int32_t *block_tables, int bt_stride,

@@ -39,3 +39,45 @@ def test_absorbed_maximum_in_the_last_tile(kf, R, heads):
         kf.kf_latent_attention(q, cache, table, ctx, c.max_ctx, c.scale, ws, out=out, lse_out=lse)
         wrong += (out != want_out).sum() + (lse != want_lse).sum()
     assert int(wrong) == 0
+
+
+# ----------------------------------------------------------------------------
+# append: ranges that are none
+# ----------------------------------------------------------------------------
+
+@pytest.mark.parametrize("start", [[0, 5, 3, 8], [-2, 3, 5, 8], [0, 2, 5, 9], [4, 4, 3, 3], [0, 8, 9, 8]])
+def test_append_ranges_that_do_not_ascend_or_leave_the_rows(kf, start):
+    """Reported, and what is written lies where some request's range puts it."""
+    g = torch.Generator().manual_seed(211)
+    lens = [3, 20, 0]
+    cache, table = ref.paged([n + 12 for n in lens], 16, 576, g)
+    new = torch.randn(8, 576, generator=g).to(torch.bfloat16)
+    d = cache.cuda()
+    kf.kf_append_latent(new.cuda(), d, table.cuda(), torch.tensor(lens, dtype=torch.int32).cuda(),
+                        row_start=torch.tensor(start, dtype=torch.int32).cuda())
+    torch.cuda.synchronize()
+    assert kf.kf_get_device_error() == kf.KF_DEVERR_CONTEXT_LEN
+    got, allowed = d.cpu().view(torch.int16), {}
+    for b, n in enumerate(lens):
+        for r in range(max(start[b], 0), min(start[b + 1], 8)):
+            p = n + r - start[b]
+            allowed[int(table[b, p // 16]), p % 16] = new[r].view(torch.int16)
+    old = cache.view(torch.int16)
+    for blk, slot in np.argwhere((got != old).any(2).numpy()):
+        assert torch.equal(got[blk, slot], allowed[int(blk), int(slot)])
+
+
+def test_append_ranges_in_order_are_no_error(kf):
+    """Many requests (more than a block's threads), some without rows."""
+    g = torch.Generator().manual_seed(212)
+    counts = [i % 3 for i in range(700)]
+    cache, table = ref.paged([c + 1 for c in counts], 16, 320, g)
+    start = np.concatenate([[0], np.cumsum(counts)])
+    new = torch.randn(int(start[-1]), 320, generator=g).to(torch.bfloat16)
+    d = cache.cuda()
+    kf.kf_append_latent(new.cuda(), d, table.cuda(), torch.ones(700, dtype=torch.int32).cuda(),
+                        row_start=torch.tensor(start, dtype=torch.int32).cuda())
+    for b, c in enumerate(counts):
+        for j in range(c):
+            cache[int(table[b, 0]), 1 + j] = new[int(start[b]) + j]
+    assert torch.equal(d.cpu().view(torch.int16), cache.view(torch.int16))
