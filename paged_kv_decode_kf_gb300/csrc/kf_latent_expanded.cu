@@ -7,8 +7,13 @@
 //   O[128 rows x v]        += P V                                 (fp16)
 // The low halves keep S, and so lse, as exact as bf16 inputs with fp32 sums allow;
 // they cost 128 of S's 320 columns. P and V as fp16 round an eighth as much as
-// bf16 would; P <= 2^8 by the lazy maximum, and fp16's least step, 2^-24 of the
-// row's largest weight, is far below what the sums keep.
+// bf16 would. P uses fp16's range whole: weights are taken relative to the running
+// maximum less 7 (base 2), so that, with the lazy maximum's 8, P <= 2^15, and fp16's
+// least step is 2^-31 of the row's largest weight or less. (Relative to the maximum
+// itself the step was 2^-24: 2^18 tokens 17.4 nats below one other were left out.) What
+// remains is the fp32 sum itself: 2^17 tokens behind one of the same value and 2^21 / 2^23
+// times their weight lose 2 / 10 % of their share to it, 2^27 times all (the absorbed
+// form, whose sums are cut over CTAs, 0 / 0 / 0.6 %).
 //
 // TMEM (512 columns): S_t, P_t over it, at 64 t; q_n of tile t (the A operand of 16
 // of S's 20 instructions: half the shared-memory reads) at 128 + 64 t; O_t at 256 +
@@ -40,6 +45,8 @@ using namespace mq5;
 
 constexpr int kRows = 128, kTok = 64;
 constexpr int kProducerWarp = 8, kIssuerWarp = 9, kThreads = 320;
+constexpr float kLift = 7.f;  // weights are 2^(score - maximum + kLift)
+static_assert(kLift + kRescaleSlack <= 15.f, "weights within fp16's range");
 
 template <int DN, int DV>
 struct EShape {
@@ -299,7 +306,7 @@ expanded_kernel(const LatentParams p, const ExpandedKV kv, int q_tiles, const __
         int64_t lim = row_ok ? (p.causal && shift + row + 1 < t_end ? shift + row + 1 : t_end) : 0;
         if (lim < 0) lim = 0;
         const float c = p.scale_log2;
-        float m = -INFINITY, l = 0.f;
+        float m = -INFINITY, l = 0.f;  // the running maximum less kLift; the weights' sum
         bool ok = true;
         for (int j = 0; j < ntiles; ++j) {
             const int64_t t0 = (int64_t)j * kTok;
@@ -341,11 +348,12 @@ expanded_kernel(const LatentParams p, const ExpandedKV kv, int q_tiles, const __
                     mx = fmaxf(mx, v);
                 }
             }
-            const bool need = mx > m + kRescaleSlack;
-            const float alpha = need ? exp2f(m - mx) : 1.f;  // m = -inf: 0
+            const bool need = mx > m + (kLift + kRescaleSlack);
+            const float lifted = mx - kLift;
+            const float alpha = need ? exp2f(m - lifted) : 1.f;  // m = -inf: 0
             if (need) {
                 l *= alpha;
-                m = mx;
+                m = lifted;
             }
             const float mu = m == -INFINITY ? 0.f : m;
             float2 ls = make_float2(0.f, 0.f);

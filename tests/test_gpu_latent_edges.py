@@ -81,3 +81,45 @@ def test_append_ranges_in_order_are_no_error(kf):
         for j in range(c):
             cache[int(table[b, 0]), 1 + j] = new[int(start[b]) + j]
     assert torch.equal(d.cpu().view(torch.int16), cache.view(torch.int16))
+
+
+# ----------------------------------------------------------------------------
+# expanded form: weights and values far below the largest
+# ----------------------------------------------------------------------------
+
+@pytest.mark.parametrize("dominant", [0.0, -1.0])
+@pytest.mark.parametrize("w,at", [(64, 0), (64, 140000), (128, (1 << 18) - 1)])
+def test_expanded_many_small_weights(kf, w, at, dominant):
+    """One token of weight 1 and 2^18 - 1 others 17.4 nats below it, 0.7 % of the sum
+    together; the one's value is 0, or the others' negated.
+
+    Bound. The small weights are 2^-25.1 of the largest and 2^7 times that in fp16, whose
+    step 2^-24 is 2^-5.9 of them: each is off by 2^-6.9 of itself at most; a value by
+    2^-11. The product's fp32 sum takes 16 products at a time; each may lose up to one
+    fp32 step, 2^-23, of the sum so far. Where all values are alike the sum grows evenly,
+    its mean half of its end: N 2^-24 = 2^-6 of the result. Where the large token comes
+    first, the sum is 1 throughout: N 2^-23 = 2^-5 of |value|, more than the others' share,
+    and the test shows the lse and that nothing else goes wrong. l takes 2^12 sums of 64,
+    each off by half a step, 2^-24: 2^-12, twice."""
+    n, R = 1 << 18, 256
+    g = torch.Generator().manual_seed(221)
+    c = Case([n], [1], 1, R, 32, seed=222, w=w)
+    c.q.zero_()
+    c.q[..., w] = 1.0
+    u = torch.randn(R, generator=g).to(torch.bfloat16)
+    c.cache[...] = torch.cat([u, torch.zeros(64, dtype=torch.bfloat16)])
+    blk = int(c.table[0, at // 32])
+    c.cache[blk, at % 32, :R] = dominant * u
+    c.cache[blk, at % 32, R] = 1.0
+    c.scale = 17.4
+    out, lse = c.run(kf)
+    # by the definition: all other tokens share one key and one value
+    v = c.w_uv[0].double().numpy() @ u.double().numpy()
+    rest = (n - 1) * np.exp(-17.4)
+    want = v * (rest + dominant) / (rest + 1.0)
+    tol = (2.0 ** -6.9 + 2.0 ** -6) * rest + 2.0 ** -11 * (rest + abs(dominant)) + 2 * 2.0 ** -12 * (rest + abs(dominant))
+    if dominant:
+        tol += 2.0 ** -5
+    err = np.abs(out[0, 0].double().numpy() - want)
+    assert np.all(err <= tol * np.abs(v)), (err / np.abs(v)).max()
+    assert abs(float(lse[0, 0]) - (17.4 + np.log1p(rest))) <= 1e-4 * 17.4
