@@ -554,9 +554,11 @@ size_t kf_latent_workspace_size(int batch, int max_query_len, int num_heads, int
  * nope_dim = v_dim = 64 or 128. Expanded keys enter the score products as pairs
  * of bf16 numbers (together 16 bits of significand, so that lse stays as exact
  * as in the absorbed form), values and softmax weights the value product as
- * fp16 (a rounding an eighth of bf16's; a weight is off by at most 2^-11 of
- * itself or 2^-32 of the row's largest, whichever is more). Its sum is fp32 over
- * all of a row's tokens: what a token adds below 2^-24 of the sum so far is lost.
+ * fp16 (a rounding an eighth of bf16's in fp16's range: a value is off by at
+ * most 2^-11 of itself or 2^-25, whichever is more, so that values far below 1
+ * lose bits and those below 2^-25 are lost; a weight by 2^-11 of itself or 2^-32
+ * of the row's largest). Its sum is fp32 over all of a row's tokens: what a token
+ * adds below 2^-24 of the sum so far is lost.
  * An expanded value above fp16's largest number (65504) sets KF_DEVERR_RANGE and
  * leaves that request's outputs unspecified.
  */

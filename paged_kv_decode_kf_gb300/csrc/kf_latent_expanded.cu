@@ -7,13 +7,13 @@
 //   O[128 rows x v]        += P V                                 (fp16)
 // The low halves keep S, and so lse, as exact as bf16 inputs with fp32 sums allow;
 // they cost 128 of S's 320 columns. P and V as fp16 round an eighth as much as
-// bf16 would. P uses fp16's range whole: weights are taken relative to the running
-// maximum less 7 (base 2), so that, with the lazy maximum's 8, P <= 2^15, and fp16's
-// least step is 2^-31 of the row's largest weight or less. (Relative to the maximum
-// itself the step was 2^-24: 2^18 tokens 17.4 nats below one other were left out.) What
-// remains is the fp32 sum itself: 2^17 tokens behind one of the same value and 2^21 / 2^23
-// times their weight lose 2 / 10 % of their share to it, 2^27 times all (the absorbed
-// form, whose sums are cut over CTAs, 0 / 0 / 0.6 %).
+// bf16 would; a value below 2^-14 is off by up to 2^-25. P uses fp16's range whole:
+// weights are taken relative to the running maximum less 7 (base 2), so that, with the
+// lazy maximum's 8, P <= 2^15, and fp16's least step is 2^-31 of the row's largest weight
+// or less. (Relative to the maximum itself the step was 2^-24: 2^18 tokens 17.4 nats below
+// one other were left out.) What remains is the fp32 sum itself: 2^17 tokens behind one of
+// the same value and 2^21 / 2^23 times their weight lose 2 / 10 % of their share to it,
+// 2^27 times all (the absorbed form, whose sums are cut over CTAs, 0 / 0 / 0.6 %).
 //
 // TMEM (512 columns): S_t, P_t over it, at 64 t; q_n of tile t (the A operand of 16
 // of S's 20 instructions: half the shared-memory reads) at 128 + 64 t; O_t at 256 +

@@ -123,3 +123,15 @@ def test_expanded_many_small_weights(kf, w, at, dominant):
     err = np.abs(out[0, 0].double().numpy() - want)
     assert np.all(err <= tol * np.abs(v)), (err / np.abs(v)).max()
     assert abs(float(lse[0, 0]) - (17.4 + np.log1p(rest))) <= 1e-4 * 17.4
+
+
+@pytest.mark.parametrize("size", [2.0 ** -10, 2.0 ** -16, 2.0 ** -22])
+def test_expanded_small_values(kf, size):
+    """Values below fp16's least normal number: off by 2^-25 at most, whatever their size."""
+    c = Case([70, 300], [9, 40], 2, 256, 16, seed=231, w=64)
+    c.w_uv = (c.w_uv.float() * size).to(torch.bfloat16)
+    out, lse = c.run(kf)
+    o, l, mag, s = ref.latent(c.q, c.q_start, c.cache, c.table, c.lens, c.scale, True, c.w_uk, c.w_uv)
+    tol = (2 * 2.0 ** -16 * s[..., None] + 2 * 2.0 ** -11 + 2e-4) * mag + 2.0 ** -25
+    assert np.all(np.abs(out.double().numpy() - o) <= tol)
+    assert np.all(np.abs(lse.double().numpy() - l) <= 2.0 ** -16 * s + 1e-4 * np.maximum(1.0, np.abs(l)))
