@@ -62,7 +62,8 @@ kf_status latent_args(LatentParams *p, const void *q, const int32_t *q_start, co
     p->num_blocks = num_blocks;
     p->bt_stride = bt_stride;
     p->max_context_len = max_context_len;
-    p->max_query_len = std::min(max_query_len, num_q_tokens);  // (what follows is sized by it)
+    // (what follows is sized by it; without ranges every request has one query)
+    p->max_query_len = q_start ? std::min(max_query_len, num_q_tokens) : 1;
     p->batch = batch;
     p->num_q_tokens = num_q_tokens;
     p->num_heads = num_heads;

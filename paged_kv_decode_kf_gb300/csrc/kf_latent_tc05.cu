@@ -10,11 +10,11 @@
 // Work. Rows come in tiles of 64 (R = 512) or 128 (R = 256), tokens in tiles of 32 or
 // 64. A unit is one row tile of one request over all its token tiles; the units of the
 // batch, laid end to end, are cut into equal runs, one a CTA (one CTA an SM: the
-// tile ring fills its shared memory); where requests have several units, one a pair
-// of CTAs, which walk it side by side. A run may start and end inside a unit; the parts of such a unit
-// go to the workspace as normalised (o, lse) partials and latent_merge joins
-// them. So a batch of any length mix keeps every SM busy to the end, at the
-// price of at most two partials a CTA.
+// tile ring fills its shared memory); where nearly all units have a partner in their
+// request, one a pair of CTAs, which walk it side by side. A run may start and end
+// inside a unit; the parts of such a unit go to the workspace as normalised (o, lse)
+// partials and latent_merge joins them. So a batch of any length mix keeps every SM
+// busy to the end, at the price of at most two partials a CTA.
 //
 // One tile: 32 or 64 rows of R + 64 bf16 arrive as TMA boxes of 16 tokens, landing as
 // 8-token groups of 128-byte-swizzled atoms (group, 64-column atom, token, column).
@@ -121,6 +121,39 @@ __device__ __forceinline__ Request request_of(const LatentParams &p, int b, bool
 __device__ __forceinline__ int64_t cost_of(const LatentParams &p, int b, int twins, bool report) {
     const Request r = request_of(p, b, report);
     return r.n * ((r.units + twins - 1) / twins);
+}
+
+// Whether pairs of CTAs pay: of `all` tiles of all units, `lone` are of requests' last, odd
+// units, where the second twin has nothing to do. 64 requests of 4K tokens, R = 512, pairs /
+// single CTAs: no lone tile, 102 / 111 us (128 rows) and 181 / 200 (256); one in 15, 102 /
+// 109; one in 9, 410 / 385; one in 5, 258 / 221; one in 3, 172 / 155; all, 90 / 64.
+__host__ __device__ constexpr bool pairs_pay(int64_t all, int64_t lone) { return lone * 12 <= all; }
+
+// CTAs that share a run, from the batch's real query counts.
+__device__ __forceinline__ int twins_of(const LatentParams &p, int64_t *sm) {
+    int64_t all = 0, lone = 0;
+    for (int b = threadIdx.x; b < p.batch; b += blockDim.x) {
+        const Request r = request_of(p, b, false);
+        all += r.n * r.units;
+        lone += r.n * (r.units & 1);
+    }
+    for (int o = 16; o; o >>= 1) {
+        all += __shfl_xor_sync(0xffffffffu, all, o);
+        lone += __shfl_xor_sync(0xffffffffu, lone, o);
+    }
+    const int warp = threadIdx.x >> 5, warps = blockDim.x / 32;
+    if ((threadIdx.x & 31) == 0) {
+        sm[2 * warp] = all;
+        sm[2 * warp + 1] = lone;
+    }
+    __syncthreads();
+    all = lone = 0;
+    for (int w = 0; w < warps; ++w) {
+        all += sm[2 * w];
+        lone += sm[2 * w + 1];
+    }
+    __syncthreads();  // `sm` is free again
+    return pairs_pay(all, lone) ? 2 : 1;
 }
 
 // One unit's part in a CTA's run: token tiles [tile0, tile0 + tiles).
@@ -297,8 +330,8 @@ __device__ __forceinline__ void store_rows(uint32_t tm, bool any, int rows, cons
 // ---------------------------------------------------------------------------
 template <int R>
 __global__ void __launch_bounds__(kThreads, 1)
-latent_kernel(const LatentParams p, const Partials part, int twins, const __grid_constant__ CUtensorMap tmap_x,
-              const __grid_constant__ CUtensorMap tmap_q) {
+latent_kernel(const LatentParams p, const Partials part, int max_twins, bool decide,
+              const __grid_constant__ CUtensorMap tmap_x, const __grid_constant__ CUtensorMap tmap_q) {
     using Sh = LShape<R>;
     constexpr int NS = Sh::kStages, NP = Sh::kPBuffers, KS = (R + kRopeDim) / 16, kN = Sh::kN, KP = kN / 16, kM = Sh::kM;
     // full[NS], empty[NS], q_full, q_empty, s_full[2], s_empty[2], p_full[2], pv_done[2], o_empty, fin[2]
@@ -350,6 +383,7 @@ latent_kernel(const LatentParams p, const Partials part, int twins, const __grid
     // wait for this kernel, and this one for it)
     if (warp == kScoreWarp) tc05::tmem_alloc(smem_u32(&tmem_slot), 512);
     if (threadIdx.x == 0) abort_flag = (*(volatile unsigned int *)p.err & KF_DEVERR_TIMEOUT) ? 1 : 0;
+    const int twins = decide ? twins_of(p, sm_loc) : max_twins;
     const int run = blockIdx.x / twins, runs = gridDim.x / twins;
     Walker walk;
     walk.twins = twins;
@@ -859,8 +893,8 @@ bool encode_cache(tc::EncodeFn fn, CUtensorMap *map, const LatentParams &p) {
 }
 
 template <int R>
-cudaError_t launch(const LatentParams &p, const Partials &part, int ctas, int twins, bool long_units, cudaStream_t stream,
-                   const CUtensorMap &mx, const CUtensorMap &mq) {
+cudaError_t launch(const LatentParams &p, const Partials &part, int ctas, int twins, bool decide, bool long_units,
+                   cudaStream_t stream, const CUtensorMap &mx, const CUtensorMap &mq) {
     using Sh = LShape<R>;
     static std::atomic<uint64_t> done{0};
     int dev = 0;
@@ -883,15 +917,16 @@ cudaError_t launch(const LatentParams &p, const Partials &part, int ctas, int tw
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    e = cudaLaunchKernelEx(&cfg, latent_kernel<R>, p, part, twins, mx, mq);
-    if (e != cudaSuccess || ctas == twins) return e;
+    e = cudaLaunchKernelEx(&cfg, latent_kernel<R>, p, part, twins, decide, mx, mq);
+    if (e != cudaSuccess || ctas == twins) return e;  // (one run: nothing is cut)
     cfg.blockDim = dim3(256);
     cfg.dynamicSmemBytes = 0;
+    const int starts = ctas - (decide ? 1 : twins);  // CTAs where a unit may start that goes on
     if (long_units) {
-        cfg.gridDim = dim3(ctas - twins, part.pitch);
+        cfg.gridDim = dim3(starts, part.pitch);
         return cudaLaunchKernelEx(&cfg, latent_merge_kernel<R, 1>, p, part);
     }
-    cfg.gridDim = dim3(ctas - twins, (part.pitch + 7) / 8);
+    cfg.gridDim = dim3(starts, (part.pitch + 7) / 8);
     return cudaLaunchKernelEx(&cfg, latent_merge_kernel<R, 8>, p, part);
 }
 
@@ -915,15 +950,22 @@ cudaError_t launch_latent(const LatentParams &p, void *workspace, int sm_count, 
     // Requests of more than one unit: two CTAs walk a run together, a unit each, so that
     // one's tiles are the other's L2 hits (64 requests of 4K tokens, 128 heads: 110 us
     // against 119, which read 550 MB from HBM for a cache of 302). With one unit a
-    // request there is nothing to share.
+    // request there is nothing to share. Where every request has as many queries as the
+    // bound (all of q's tokens) that is known here, else the kernel looks (0.8 us).
     const int M = unit_rows(p.latent_dim);
-    const int64_t rows_max = (int64_t)p.max_query_len * p.num_heads;
-    const int twins = rows_max > M ? 2 : 1;
-    // no more runs than the batch can have pieces of 64 tokens (1 request of 777 tokens, 16 heads:
-    // 16.7 us with 13 runs, 18.6 with 25 of 32 tokens)
-    const int64_t groups = (int64_t)p.batch * ((rows_max + twins * M - 1) / (twins * M));
-    const int64_t pieces = groups * std::max<int64_t>(1, ((int64_t)p.max_context_len + 63) / 64);
+    const int64_t rows_max = (int64_t)p.max_query_len * p.num_heads, units_max = (rows_max + M - 1) / M;
+    const bool uniform = (int64_t)p.batch * p.max_query_len == p.num_q_tokens;
+    const int twins = units_max > 1 && (!uniform || pairs_pay(units_max, units_max & 1)) ? 2 : 1;
+    // No more units (groups of twins) than the bound, and than all query rows, allow; and no
+    // more runs than these have pieces of 64 tokens (1 request of 777 tokens, 16 heads:
+    // 16.7 us with 13 runs, 18.6 with 25 of 32 tokens).
+    auto groups_of = [&](int64_t rows) {
+        return std::min<int64_t>((int64_t)p.batch * ((rows_max + rows - 1) / rows),
+                                 p.batch + (int64_t)p.num_q_tokens * p.num_heads / rows);
+    };
+    const int64_t pieces = groups_of(twins * M) * std::max<int64_t>(1, ((int64_t)p.max_context_len + 63) / 64);
     const int ctas = twins * (int)std::min<int64_t>(std::max(1, sm_count / twins), pieces);
+    const bool decide = twins == 2 && !uniform && ctas > 2;
     Partials part;
     part.pitch = (int)row_pitch(p.max_query_len, p.num_heads, p.latent_dim);
     part.o = static_cast<float *>(workspace);
@@ -934,9 +976,9 @@ cudaError_t launch_latent(const LatentParams &p, void *workspace, int sm_count, 
     // few units are cut over many CTAs each: one row a merge block, its warps share
     // the partials; many units have two or three partials: one warp a row (1 request of
     // 30K tokens, 16 heads: 31 us against 76; 32 requests of 8K: 73 against 70)
-    const bool long_units = groups * twins * 8 < ctas;
-    return p.latent_dim == 512 ? launch<512>(p, part, ctas, twins, long_units, stream, mx, mq)
-                               : launch<256>(p, part, ctas, twins, long_units, stream, mx, mq);
+    const bool long_units = groups_of(M) * 8 < ctas;
+    return p.latent_dim == 512 ? launch<512>(p, part, ctas, twins, decide, long_units, stream, mx, mq)
+                               : launch<256>(p, part, ctas, twins, decide, long_units, stream, mx, mq);
 }
 
 }  // namespace kf

@@ -135,3 +135,37 @@ def test_expanded_small_values(kf, size):
     tol = (2 * 2.0 ** -16 * s[..., None] + 2 * 2.0 ** -11 + 2e-4) * mag + 2.0 ** -25
     assert np.all(np.abs(out.double().numpy() - o) <= tol)
     assert np.all(np.abs(lse.double().numpy() - l) <= 2.0 ** -16 * s + 1e-4 * np.maximum(1.0, np.abs(l)))
+
+
+# ----------------------------------------------------------------------------
+# host bounds above the real sizes
+# ----------------------------------------------------------------------------
+
+@pytest.mark.parametrize("R,heads", [(512, 20), (512, 64), (256, 20)])
+def test_absorbed_work_is_cut_by_the_real_query_counts(kf, R, heads):
+    """A bound of several draft tokens where requests bring one: the bits of the exact
+    bound, so the same runs on the same CTAs."""
+    lens = [900 + 37 * i for i in range(64)]
+    c = Case(lens, [1] * 64, heads, R, seed=251 + heads)
+    want = c.run(kf)
+    c.check(*want)
+    for bound in (4, 64, 2 ** 31 - 1):
+        c.max_q = bound
+        got = c.run(kf)
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1]), bound
+        got = c.run(kf, q_start=False)
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1]), bound
+
+
+@pytest.mark.parametrize("counts", [[3] * 9, [1, 4, 1, 1, 4, 1, 0, 1, 2], [4] * 8 + [1], [2, 2, 2, 1, 2, 2, 2, 2, 2],
+                                    [4, 0, 0, 0, 0, 0, 0, 0, 0]])
+@pytest.mark.parametrize("R,heads", [(512, 40), (256, 64)])
+def test_absorbed_odd_and_even_units(kf, R, heads, counts):
+    """Requests of one, two, three and more units in one batch, cut over CTAs."""
+    lens = [700, 33, 1500, 64, 5, 260, 90, 2100, 31]
+    c = Case(lens, counts, heads, R, seed=261 + sum(counts))
+    out, lse = c.run(kf)
+    c.check(out, lse)
+    c.max_q = 9
+    out, lse = c.run(kf, causal=False)
+    c.check(out, lse, False)
