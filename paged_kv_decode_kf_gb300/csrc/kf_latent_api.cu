@@ -117,7 +117,8 @@ kf_status accumulate_impl(const void *q, const int32_t *q_start, const void *k_c
     p.score_stride = score_stride;
     p.bt_stride = bt_stride;
     p.max_context_len = max_context_len;
-    p.max_query_len = std::min(max_query_len, num_q_tokens);
+    // (without ranges every request has one query)
+    p.max_query_len = q_start ? std::min(max_query_len, num_q_tokens) : std::min(max_query_len, 1);
     p.batch = batch;
     p.num_q_tokens = num_q_tokens;
     p.num_q_heads = num_q_heads;
