@@ -8,6 +8,25 @@ from test_gpu_evict import _acc_inputs, _evict_case, _run_acc, kf, no_device_err
 pytestmark = pytest.mark.gpu
 
 
+@pytest.mark.parametrize("alias", [False, True])
+@pytest.mark.parametrize("with_pos", [False, True])
+@pytest.mark.parametrize("keep", [399990, 1000])
+def test_evict_keys_beyond_shared_memory(kf, alias, with_pos, keep):
+    """Keys computed again in every pass, in place and with positions, beside short
+    requests; few moves and many."""
+    _evict_case(kf, [400001, 30, 1200], keep, 4, 5, 16, 1, with_pos, 21, alias=alias)
+
+
+@pytest.mark.parametrize("hq,hkv,D", [(20, 10, 128), (9, 9, 64), (48, 24, 64), (16, 16, 128)])
+@pytest.mark.parametrize("fp8", [False, True])
+def test_accumulate_windows_of_many_heads(kf, fp8, hq, hkv, D):
+    """More KV heads than a block has warps: heads take turns."""
+    lens, counts = [140, 7, 65, 300], [33, 7, 12, 0]
+    a = _acc_inputs(lens, counts, hq, hkv, D, 16, fp8, seed=31 + hq)
+    _run_acc(kf, a, lens, counts, True)
+    _run_acc(kf, a, lens, counts, False)
+
+
 @pytest.mark.parametrize("fp8", [False, True])
 def test_accumulate_one_query_whatever_the_bound(kf, fp8):
     """Without q_start every request has one query, whatever max_query_len says: the same

@@ -137,6 +137,14 @@ def test_expanded_small_values(kf, size):
     assert np.all(np.abs(lse.double().numpy() - l) <= 2.0 ** -16 * s + 1e-4 * np.maximum(1.0, np.abs(l)))
 
 
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("R,w,bs", [(256, 128, 16), (256, 128, 32), (512, 64, 16)])
+def test_expanded_every_width_of_latent_and_head(kf, causal, R, w, bs):
+    c = Case([150, 40, 1, 0, 129, 300], [150, 7, 1, 0, 128, 33], 3, R, bs, seed=241 + w, w=w)
+    out, lse = c.run(kf, causal=causal)
+    c.check(out, lse, causal)
+
+
 # ----------------------------------------------------------------------------
 # host bounds above the real sizes
 # ----------------------------------------------------------------------------
