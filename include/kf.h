@@ -509,7 +509,8 @@ kf_status kf_append_latent(const void *latent_new, const int32_t *row_start, voi
  *                 request (num_q_tokens == batch)
  *   context_lens  int32 [batch], tokens in the cache, the queries' own included
  *   causal        1: query j sees tokens [0, L_b - C_b + j]; 0: all L_b tokens
- *   max_context_len, max_query_len  host-side bounds of L_b and C_b
+ *   max_context_len, max_query_len  host-side bounds of L_b and C_b (without
+ *                 q_start C_b is 1, and a larger max_query_len changes nothing)
  *   workspace     device scratch of kf_latent_workspace_size() bytes, 16-byte
  *                 aligned, any contents. Calls that share one must not overlap
  *                 on the GPU.
@@ -537,8 +538,9 @@ kf_status kf_latent_attention(const void *q, const int32_t *q_start, const void 
                               float scale, void *workspace, size_t workspace_bytes, void *out,
                               kf_dtype out_dtype, float *lse_out, kf_stream_t stream);
 
-/* Workspace bytes of kf_latent_attention on the CURRENT device; 0 if that device
- * cannot be queried or the arguments are invalid. */
+/* Workspace bytes of kf_latent_attention on the CURRENT device, whatever the batch
+ * (which is checked alone); 0 if that device cannot be queried or the arguments
+ * are invalid. */
 size_t kf_latent_workspace_size(int batch, int max_query_len, int num_heads, int latent_dim);
 
 /*
@@ -573,7 +575,9 @@ kf_status kf_latent_attention_expanded(const void *q, const int32_t *q_start,
                                        size_t workspace_bytes, void *out, kf_dtype out_dtype,
                                        float *lse_out, kf_stream_t stream);
 
-/* Workspace bytes of kf_latent_attention_expanded; 0 if the arguments are invalid. */
+/* Workspace bytes of kf_latent_attention_expanded, 4 nope_dim + 2 v_dim a head and
+ * token of batch * max_context_len (num_q_tokens is checked alone): 13 GB for one
+ * request of 128K tokens and 128 heads of 128. 0 if the arguments are invalid. */
 size_t kf_latent_expanded_workspace_size(int batch, int num_q_tokens, int max_context_len,
                                          int num_heads, int nope_dim, int v_dim);
 
@@ -583,8 +587,10 @@ size_t kf_latent_expanded_workspace_size(int batch, int num_q_tokens, int max_co
  *
  * A cache bounded to `keep` tokens a request drops the tokens that later
  * queries have looked at least. kf_accumulate_attention adds up, per cached
- * token, the softmax weight it received; kf_evict_tokens picks who stays and
- * closes the gaps in place, for any paged cache (K/V in bf16 or E4M3, latent).
+ * token, the softmax weight it received, over a cache of keys (bf16 or E4M3);
+ * kf_evict_tokens picks who stays and closes the gaps in place, by any scores
+ * and for any paged cache (K/V in bf16 or E4M3, latent). No call here yields the
+ * weights of latent attention: the scores of a latent cache are the caller's.
  */
 
 /*
@@ -653,7 +659,8 @@ kf_status kf_accumulate_attention_fp8(const void *q, const int32_t *q_start, con
  *                     sequence's length is L
  *   keep >= 1, sink + recent <= keep
  *   context_lens_out  int32 [batch]; may be context_lens
- *   workspace         kf_evict_workspace_size() bytes, 16-byte aligned, any contents
+ *   workspace         kf_evict_workspace_size() bytes, 16-byte aligned, any contents.
+ *                     Calls that share one must not overlap on the GPU.
  *
  * Host errors: null pointers, sizes out of range, part of the three position
  * arrays -> KF_ERR_INVALID; row_bytes not a multiple of 16 (or above 1 MiB),

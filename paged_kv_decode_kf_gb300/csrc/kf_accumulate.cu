@@ -40,7 +40,8 @@ constexpr int kWarps = 4;  // warps a CTA
 // 16-token tiles a warp holds, and CTAs an SM: as many keys in flight either way, and
 // enough of them a warp to pay for q's conversion (64 requests of 4K, bf16: 90 us with
 // 2 tiles x 3 CTAs, 93 with 2 x 4, 96 with 1 x 6 and 4 x 2; ragged E4M3: 146 us with
-// 4 x 3, 155 with 2 x 4, 199 with 1 x 6, and 136 once L2 fetches keys by 256 bytes).
+// 4 x 3, 155 with 2 x 4, 199 with 1 x 6, and 136 once L2 fetches keys by 256 bytes). Three
+// CTAs leave a thread 168 registers: E4M3 at D = 128 spills 60 bytes there.
 template <bool KV8>
 struct Held {
     static constexpr int kTiles = KV8 ? 4 : 2, kCtas = 3;
@@ -330,9 +331,11 @@ accumulate_kernel(const AccumulateParams p) {
 
 // Windows of queries (more than eight columns a KV head) over E4M3 keys: one CTA a run of 64 tokens,
 // its eight warps split the (KV head, column group) pairs, so that the tokens' keys
-// are held while the columns pass (128 registers at D = 128) and q, which every CTA
-// reads whole, is read once per 64 tokens. The next group's q is asked for before this
-// one's products. The warps' sums meet in shared memory, in warp order.
+// are held while the columns pass (64 registers at D = 128, of 214: one CTA an SM) and q,
+// which every CTA reads whole, is read once per 64 tokens. The next group's q is asked for
+// before this one's products. The warps' sums meet in shared memory, in warp order. What
+// bounds it: keys widened again for every eight columns, and mma.sync: 4 requests of
+// 4K-12K tokens, 32 / 64 queries of 32 / 8 heads: 62 / 110 us (bf16 keys on tcgen05: 22 / 35).
 constexpr int kWinWarps = 8, kWinTiles = 4;
 
 template <int D>
@@ -423,9 +426,10 @@ accumulate_window_kernel(const AccumulateParams p) {
 template <int D, bool KV8>
 cudaError_t launch(const AccumulateParams &p, int sm_count, cudaStream_t stream, void *encode_fn) {
     // Columns a KV head: up to eight are one pass of the row kernel; more keep the keys
-    // while the columns pass, bf16 ones on tcgen05 (E4M3 keys need fp16 products, and
-    // tcgen05 takes no fp16 operand beside an 8-bit one). 64 requests of 4K tokens, 8 / 16
-    // / 32 columns: 94 / 110 / 152 us with the row kernel, 106 / 107 / 107 on tcgen05.
+    // while the columns pass, bf16 ones on tcgen05 (E4M3 ones would have to be widened to
+    // bf16 in shared memory for it, which is not built: accumulate_window_kernel). 64
+    // requests of 4K tokens, 8 / 16 / 32 columns: 94 / 110 / 152 us with the row kernel, 106
+    // / 107 / 107 on tcgen05.
     const int64_t cols = (int64_t)p.max_query_len * (p.num_q_heads / p.num_kv_heads);
     if (!KV8 && cols > 8 && p.num_q_tokens > 0) return launch_accumulate_tc05(p, sm_count, stream, encode_fn);
     const int64_t tiles = (int64_t)p.batch * ((p.max_context_len + 15) / 16);

@@ -71,8 +71,9 @@ cudaError_t launch_append_latent(const uint16_t *rows, const int32_t *row_start,
                                  int num_rows, int row_dim, int block_size, int64_t num_blocks, unsigned int *err,
                                  cudaStream_t stream);
 
-// Absorbed form: partial slots in `workspace` (latent_slots floats, see kf_latent.cu).
-size_t latent_workspace_bytes(int batch, int max_query_len, int num_heads, int latent_dim, int sm_count);
+// Absorbed form: the partials of cut units in `workspace` (their o, lse and Cut records, two
+// slots an SM: kf_latent_tc05.cu).
+size_t latent_workspace_bytes(int max_query_len, int num_heads, int latent_dim, int sm_count);
 cudaError_t launch_latent(const LatentParams &p, void *workspace, int sm_count, cudaStream_t stream, void *encode_fn);
 
 // Expanded form: K_nope and V of every token in `workspace`.
@@ -81,8 +82,7 @@ struct LatentWeights {
     const uint16_t *w_uv;  // bf16 [H, v, R]
     int nope, v;
 };
-size_t latent_expanded_workspace_bytes(int batch, int num_q_tokens, int max_context_len, int num_heads, int nope,
-                                       int v);
+size_t latent_expanded_workspace_bytes(int batch, int max_context_len, int num_heads, int nope, int v);
 cudaError_t launch_latent_expanded(const LatentParams &p, const LatentWeights &w, void *workspace, int sm_count,
                                    cudaStream_t stream, void *encode_fn);
 

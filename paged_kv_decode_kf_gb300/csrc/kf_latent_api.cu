@@ -168,7 +168,7 @@ size_t kf_latent_workspace_size(int batch, int max_query_len, int num_heads, int
     unsigned int *err = nullptr;
     int sms = 0;
     if (device_facts(&err, &sms) != cudaSuccess) return 0;
-    return latent_workspace_bytes(batch, max_query_len, num_heads, latent_dim, sms);
+    return latent_workspace_bytes(max_query_len, num_heads, latent_dim, sms);
 }
 
 kf_status kf_latent_attention(const void *q, const int32_t *q_start, const void *latent_cache,
@@ -184,7 +184,7 @@ kf_status kf_latent_attention(const void *q, const int32_t *q_start, const void 
     if (st != KF_OK || batch == 0 || num_q_tokens == 0 || max_query_len == 0) return st;
     int sms = 0;
     if (device_facts(&p.err, &sms) != cudaSuccess) return KF_ERR_CUDA;
-    if (workspace_bytes < latent_workspace_bytes(batch, max_query_len, num_heads, latent_dim, sms))
+    if (workspace_bytes < latent_workspace_bytes(max_query_len, num_heads, latent_dim, sms))
         return KF_ERR_INVALID;
     void *fn = tensor_map_encoder();
     if (!fn) return KF_ERR_CUDA;
@@ -194,7 +194,7 @@ kf_status kf_latent_attention(const void *q, const int32_t *q_start, const void 
 size_t kf_latent_expanded_workspace_size(int batch, int num_q_tokens, int max_context_len, int num_heads, int nope_dim,
                                          int v_dim) {
     if (batch < 0 || num_q_tokens < 0 || max_context_len < 0 || num_heads < 1 || nope_dim < 1 || v_dim < 1) return 0;
-    return latent_expanded_workspace_bytes(batch, num_q_tokens, max_context_len, num_heads, nope_dim, v_dim);
+    return latent_expanded_workspace_bytes(batch, max_context_len, num_heads, nope_dim, v_dim);
 }
 
 kf_status kf_latent_attention_expanded(const void *q, const int32_t *q_start, const void *latent_cache,
@@ -214,8 +214,7 @@ kf_status kf_latent_attention_expanded(const void *q, const int32_t *q_start, co
     if (!((nope_dim == 64 && v_dim == 64) || (nope_dim == 128 && v_dim == 128))) return KF_ERR_UNSUPPORTED;
     // rows of the expanded keys and values fit the 31-bit TMA coordinates
     if (((int64_t)max_context_len + 127) / 128 * 128 * batch * num_heads > 0x7fffffff) return KF_ERR_UNSUPPORTED;
-    if (workspace_bytes <
-        latent_expanded_workspace_bytes(batch, num_q_tokens, max_context_len, num_heads, nope_dim, v_dim))
+    if (workspace_bytes < latent_expanded_workspace_bytes(batch, max_context_len, num_heads, nope_dim, v_dim))
         return KF_ERR_INVALID;
     int sms = 0;
     if (device_facts(&p.err, &sms) != cudaSuccess) return KF_ERR_CUDA;

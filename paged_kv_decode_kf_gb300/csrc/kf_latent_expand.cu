@@ -18,7 +18,7 @@
 //
 // The epilogue's thread owns a token: K as hi = bf16(k) and lo = bf16(k - hi), V as
 // fp16, through 4 KB of shared memory a warp, so that a store covers whole 128-byte
-// lines. A value above fp16's range sets KF_DEVERR_RANGE.
+// lines (with heads of 128 it spills 16 bytes of its 168 registers). A value above fp16's range sets KF_DEVERR_RANGE.
 //   warps 0-3 / 4-7  epilogue of the even / odd heads of the run (their accumulator)
 //   warp 8           TMA producer
 //   warp 9           even CTA: MMA issuer; odd CTA: tells the even one what has landed

@@ -479,8 +479,7 @@ size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
 
 }  // namespace
 
-size_t latent_expanded_workspace_bytes(int batch, int num_q_tokens, int max_context_len, int num_heads, int nope,
-                                       int v) {
+size_t latent_expanded_workspace_bytes(int batch, int max_context_len, int num_heads, int nope, int v) {
     const size_t rows = (size_t)batch * token_cap(max_context_len) * num_heads;
     return align256(rows * 2 * nope * 2) + align256(rows * v * 2);
 }

@@ -936,7 +936,7 @@ namespace {
 size_t al256(size_t x) { return (x + 255) & ~(size_t)255; }
 }  // namespace
 
-size_t latent_workspace_bytes(int batch, int max_query_len, int num_heads, int latent_dim, int sm_count) {
+size_t latent_workspace_bytes(int max_query_len, int num_heads, int latent_dim, int sm_count) {
     sm_count = std::max(sm_count, 2);
     const size_t rows = 2 * (size_t)sm_count * row_pitch(max_query_len, num_heads, latent_dim);
     return al256(rows * latent_dim * 4) + al256(rows * 4) + sm_count * sizeof(Cut);
