@@ -177,3 +177,46 @@ def test_absorbed_odd_and_even_units(kf, R, heads, counts):
     c.max_q = 9
     out, lse = c.run(kf, causal=False)
     c.check(out, lse, False)
+
+
+@pytest.mark.parametrize("R,heads", [(512, 40), (256, 64)])
+def test_absorbed_graph_follows_query_counts(kf, R, heads):
+    """A call captured with one set of query counts, replayed with others: requests of
+    one, two and three units, with and without rows that no request owns."""
+    lens = [700, 33, 1500, 64, 5, 260, 90]
+    first = Case(lens, [4] * 7, heads, R, seed=271)
+    q, cache, table, ctx, qs = first.dev()
+    ws = kf.make_latent_workspace(7, 5, heads, R)
+    for bound, captured in ((4, [4] * 7), (5, [1] * 7)):      # every query a request's; and not
+        out = torch.empty(28, heads, R, device="cuda")
+        lse = torch.empty(28, heads, device="cuda")
+        qs.copy_(torch.tensor(np.concatenate([[0], np.cumsum(captured)]), dtype=torch.int32))
+
+        def step():
+            kf.kf_latent_attention(q, cache, table, ctx, 1500, first.scale, ws, q_start=qs, max_query_len=bound,
+                                   out=out, lse_out=lse)
+        step()
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            step()
+        for counts in ([1] * 7, [4] * 7, [2, 2, 2, 2, 2, 2, 1], [1, 3, 0, 4, 4, 4, 1], [0] * 7):
+            first.q_start = torch.tensor(np.concatenate([[0], np.cumsum(counts)]), dtype=torch.int32)
+            qs.copy_(first.q_start)
+            out.fill_(77.0)
+            lse.fill_(77.0)
+            graph.replay()
+            torch.cuda.synchronize()
+            first.check(out.cpu(), lse.cpu())
+
+
+@pytest.mark.parametrize("R", [512, 256])
+@pytest.mark.parametrize("lens,counts,heads,gap,bound", [
+    ([40], [1], 40, 2, 4), ([64], [3], 64, 0, 3), ([1], [1], 128, 0, 1), ([65], [2], 128, 1, 9), ([0], [2], 128, 0, 2),
+    ([30, 0], [1, 0], 64, 3, 7), ([200], [9], 128, 0, 9)])
+def test_absorbed_few_pairs(kf, R, lens, counts, heads, gap, bound):
+    """One pair of CTAs or two, with units for one CTA of a pair or for both."""
+    c = Case(lens, counts, heads, R, seed=281 + heads, gap=gap)
+    c.max_q = bound
+    out, lse = c.run(kf)
+    c.check(out, lse)
