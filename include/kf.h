@@ -510,7 +510,8 @@ kf_status kf_append_latent(const void *latent_new, const int32_t *row_start, voi
  *   context_lens  int32 [batch], tokens in the cache, the queries' own included
  *   causal        1: query j sees tokens [0, L_b - C_b + j]; 0: all L_b tokens
  *   max_context_len, max_query_len  host-side bounds of L_b and C_b (without
- *                 q_start C_b is 1, and a larger max_query_len changes nothing)
+ *                 q_start C_b is 1, and a larger max_query_len changes nothing; a
+ *                 max_query_len of 0 does nothing, as an empty batch or q)
  *   workspace     device scratch of kf_latent_workspace_size() bytes, 16-byte
  *                 aligned, any contents. Calls that share one must not overlap
  *                 on the GPU.
