@@ -186,7 +186,7 @@ def _prepare_prompt(st, case, gen):
     # one projection's output: a token's queries, keys and values side by side
     st["qkv"] = _normal((T, Hq + 2 * Hkv, D), gen)
     st["qkv"][:, :Hq] *= 1.5
-    st["start"], st["max_len"] = _int32(_starts(lens)), int(lens.max())
+    st["start"] = _int32(_starts(lens))
     st["scale"] = D ** -0.5
     dtype = torch.bfloat16 if case["out"] == "bf16" else torch.float32
     st["out"] = torch.empty((T, Hq, D), dtype=dtype, device="cuda")
@@ -303,15 +303,16 @@ def _attend(q, k, v, seen, scale):
 
 def _run_prompt(st):
     case = st["case"]
+    lens = _lens(case)
     Hq, Hkv = case["q_heads"], case["kv_heads"]
     q, k, v = st["qkv"].split([Hq, Hkv, Hkv], 1)
     if own:
         from paged_kv_decode_kf_gb300 import kf
-        kf.kf_prompt_attention(q, k, v, st["start"], st["max_len"], st["scale"], causal=case["causal"],
+        kf.kf_prompt_attention(q, k, v, st["start"], int(lens.max()), st["scale"], causal=case["causal"],
                                out=st["out"], lse_out=st["lse"])
         return st["out"], st["lse"]
     at = 0
-    for L in _lens(case).tolist():
+    for L in lens.tolist():
         kf32, vf32 = k[at:at + L].float(), v[at:at + L].float()
         for i in range(0, L, 2048):
             n = min(2048, L - i)
