@@ -6,14 +6,17 @@
 // blocks; with off_b the sum of need over the requests before it, its i-th new block is
 // the pool's list[free - 1 - (off_b + i)]. A request grows if off_b + need_b <= free: the
 // needs of all requests up to it count, so none behind the first that does not fit does.
+// Rows belong to one request: a range that leaves the rows, or starts before the largest end
+// of the ranges ahead of it that do not, is refused. That end, which only rises, is also
+// what a row's request is searched by, so that a refused range hides no other's rows.
 // release: the blocks behind ceil(target / bs), request by request in ascending order,
 // go back so that entry j of `total` lands at list[free + total - 1 - j]: the exact
 // opposite of an extend between the same lengths.
 //
 // Rows are the unit of work: a row finds its request and from off_b its block, and the
 // row at a new block's first position (every new block has one) writes the table entry.
-// So no CTA waits for another: each sums the needs of the whole batch by itself (three
-// words a request, from L2), which replaces a launch between the sums and the rows: extend and
+// So no CTA waits for another: each finds the ends and the needs of the whole batch by itself
+// (three words a request, from L2), which replaces a launch between the sums and the rows: extend and
 // release together 7.3 us for 64 requests of one row, 8.2 for 33 prompts of 37000 rows. The
 // last CTA to finish (a ticket in the pool's header) moves the pool's count and writes
 // the lengths, which may overwrite those that the others read.
@@ -33,16 +36,26 @@ struct Need {
     int64_t len, held, blocks;
 };
 
-__device__ __forceinline__ Need need_of(const PoolArgs &a, int b, bool report) {
-    Need n;
-    int64_t s = b, e = b + 1;
+// Request b's rows [s, e); false where they leave the array's.
+__device__ __forceinline__ bool rows_of(const PoolArgs &a, int b, int64_t &s, int64_t &e) {
+    s = b;
+    e = b + 1;
     if (a.row_start) {
         s = a.row_start[b];
         e = a.row_start[b + 1];
     }
+    return s >= 0 && e >= s && e <= a.num_rows;
+}
+
+// `end`: the largest end of the rows of the requests before b; b's counts from here on.
+__device__ __forceinline__ Need need_of(const PoolArgs &a, int b, bool report, int64_t &end) {
+    Need n;
+    int64_t s, e;
+    const bool inside = rows_of(a, b, s, e), apart = inside && s >= end;
+    if (inside && e > end) end = e;
     n.len = a.before[b];
     unsigned int bad = 0;
-    if (s < 0 || e < s || e > a.num_rows || n.len < 0) bad = KF_DEVERR_CONTEXT_LEN;
+    if (!apart || n.len < 0) bad = KF_DEVERR_CONTEXT_LEN;
     else if (n.len + (e - s) > (int64_t)a.bt_stride * a.block_size) bad = KF_DEVERR_APPEND_POS;
     if (bad) {
         if (report) raise_error(a.err, bad);
@@ -90,6 +103,22 @@ __device__ __forceinline__ int64_t scan_before(int64_t mine, int64_t *sm_warp, i
     return before;
 }
 
+// The largest of `mine` (none below 0) over the threads before this one.
+__device__ __forceinline__ int64_t max_before(int64_t mine, int64_t *sm_warp) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    int64_t v = mine;
+    for (int o = 1; o < 32; o <<= 1) {
+        const int64_t y = __shfl_up_sync(0xffffffffu, v, o);
+        if (lane >= o) v = max(v, y);
+    }
+    if (lane == 31) sm_warp[warp] = v;
+    v = __shfl_up_sync(0xffffffffu, v, 1);
+    if (lane == 0) v = 0;
+    __syncthreads();
+    for (int w = 0; w < warp; ++w) v = max(v, sm_warp[w]);
+    return v;
+}
+
 // The free count, inside the list whatever the word holds.
 __device__ __forceinline__ int64_t free_of(const PoolArgs &a, bool report) {
     const int64_t f = *(volatile int32_t *)a.pool;
@@ -115,8 +144,9 @@ __device__ __forceinline__ bool last_cta(int32_t *pool, int *sm_last) {
 
 __global__ void __launch_bounds__(kThreads)
 extend_kernel(const PoolArgs a) {
-    __shared__ int64_t sm_warp[kThreads / 32];
-    __shared__ int64_t sm_off[kThreads], sm_first[kThreads];  // of a thread's first request
+    __shared__ int64_t sm_warp[kThreads / 32], sm_warp_end[kThreads / 32];
+    // Of a thread's first request: the blocks before it, and the largest end of the rows before it.
+    __shared__ int64_t sm_off[kThreads], sm_end[kThreads];
     __shared__ unsigned long long sm_taken;
     __shared__ int sm_last;
     const int tid = threadIdx.x;
@@ -125,14 +155,13 @@ extend_kernel(const PoolArgs a) {
     const int chunks = (a.batch + per - 1) / per;
     const int b0 = min(tid * per, a.batch), b1 = min(b0 + per, a.batch);
     const int64_t free = free_of(a, report && tid == 0);
-    int64_t mine = 0;
-    sm_first[tid] = 0x7fffffffffffffffll;
-    for (int b = b0; b < b1; ++b) {
-        const Need n = need_of(a, b, report);
-        if (b == b0) sm_first[tid] = n.first;
-        mine += n.blocks;
-    }
-    int64_t total;
+    int64_t mine = 0, total, last = 0, s, e;
+    for (int b = b0; b < b1; ++b)
+        if (rows_of(a, b, s, e)) last = max(last, e);
+    const int64_t ahead = max_before(last, sm_warp_end);
+    sm_end[tid] = ahead;
+    int64_t end = ahead;
+    for (int b = b0; b < b1; ++b) mine += need_of(a, b, report, end).blocks;
     sm_off[tid] = scan_before(mine, sm_warp, total);
     if (tid == 0) sm_taken = 0;
     __syncthreads();
@@ -140,16 +169,17 @@ extend_kernel(const PoolArgs a) {
     const int32_t *list = a.pool + KF_POOL_HEADER;
     const int shift = block_shift(a.block_size);
     for (int64_t r = (int64_t)blockIdx.x * kThreads + tid; r < a.num_rows; r += (int64_t)gridDim.x * kThreads) {
-        int lo = 0, hi = chunks;  // the last chunk that starts at or before r
+        int lo = 0, hi = chunks;  // the last chunk that no rows behind r come ahead of
         while (hi - lo > 1) {
             const int mid = (lo + hi) >> 1;
-            if (sm_first[mid] <= r) lo = mid;
+            if (sm_end[mid] <= r) lo = mid;
             else hi = mid;
         }
         int64_t off = sm_off[lo];
+        end = sm_end[lo];
         int64_t slot = -1, pos = -1;
         for (int b = lo * per; b < min(lo * per + per, a.batch); ++b) {
-            const Need n = need_of(a, b, false);
+            const Need n = need_of(a, b, false, end);
             if (r >= n.first && r < n.first + n.rows) {
                 if (off + n.blocks <= free) {
                     pos = n.len + (r - n.first);
@@ -171,8 +201,9 @@ extend_kernel(const PoolArgs a) {
     if (!last_cta(a.pool, &sm_last)) return;
     int64_t off = sm_off[tid], taken = 0;
     bool short_of = false;
+    end = ahead;
     for (int b = b0; b < b1; ++b) {
-        const Need n = need_of(a, b, false);
+        const Need n = need_of(a, b, false, end);
         const bool fits = off + n.blocks <= free;
         off += n.blocks;
         if (fits) taken = off;
