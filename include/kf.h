@@ -943,7 +943,7 @@ kf_status kf_get_device_error(unsigned int *flags, kf_stream_t stream);
  * The TMA-fed kernels wait on shared-memory mbarriers, each wait bounded: a
  * wait that gives up sets KF_DEVERR_TIMEOUT in the error word and the kernel
  * returns instead of hanging. This call launches one block that waits, with
- * the same bounded wait at a short limit (2^16 polls, milliseconds), on a
+ * the same bounded wait at a short limit (2^16 polls, a quarter of a second), on a
  * barrier that nothing completes, so it always sets KF_DEVERR_TIMEOUT; a
  * following kf_get_device_error reports it, and the context stays usable.
  * Returns KF_ERR_CUDA if the launch fails.

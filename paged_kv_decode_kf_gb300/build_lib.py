@@ -33,6 +33,7 @@ HEADERS = [os.path.join(CSRC, "kf_internal.cuh"), os.path.join(CSRC, "kf_decode_
            os.path.join(CSRC, "kf_tc05_ops.cuh"), os.path.join(CSRC, "kf_evict.cuh"),
            os.path.join(CSRC, "kf_prompt.cuh"), os.path.join(CSRC, "kf_tree.cuh"),
            os.path.join(CSRC, "kf_tables.cuh"), os.path.join(CSRC, "kf_row_tile.cuh"),
+           os.path.join(CSRC, "kf_wait.cuh"),
            os.path.join(ROOT, "include", "kf.h")]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ARCH + ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-I" + os.path.join(ROOT, "include")]

@@ -56,6 +56,7 @@
 
 #include "kf_prompt.cuh"
 #include "kf_row_tile.cuh"
+#include "kf_wait.cuh"
 
 namespace kf {
 namespace {
@@ -265,14 +266,10 @@ prompt_kernel(const PromptParams p, const __grid_constant__ CUtensorMap tmap_q,
         __syncwarp();
         if (lane == 0) mbar_arrive(bar);
     };
-    // A wait that may last as long as a unit does (seconds, for the longest prompts): as many
-    // bounded waits, given up early if another role has.
+    // A wait that may last as long as a unit does; given up early if another role has (kf_wait.cuh).
     auto long_wait = [&](uint32_t bar, uint32_t parity) {
-        for (int i = 0; i < 1024; ++i) {
-            if (warp_wait(bar, parity)) return true;
-            if (__any_sync(0xffffffffu, abort_flag != 0)) return false;
-        }
-        return false;
+        return wait_in_slices([&] { return (bool)__all_sync(0xffffffffu, mbar_wait(bar, parity, kPollsASlice)); },
+                              [&] { return (bool)__any_sync(0xffffffffu, abort_flag != 0); });
     };
     // The k-th unit of this CTA; false behind the last one, or where a wait gave up (`ok`).
     auto next_unit = [&](int k, Unit &u, bool &ok) {

@@ -52,6 +52,7 @@
 #include "kf_row_tile.cuh"
 #include "kf_runs.cuh"
 #include "kf_tree.cuh"
+#include "kf_wait.cuh"
 
 namespace kf {
 namespace {
@@ -271,14 +272,10 @@ tree_kernel(const TreeParams p, const Partials part, const __grid_constant__ CUt
         __syncwarp();
         if (lane == 0) mbar_arrive(bar);
     };
-    // A wait that may last as long as a part does: as many bounded waits, given up early if
-    // another role has.
+    // A wait that may last as long as a part does; given up early if another role has (kf_wait.cuh).
     auto long_wait = [&](uint32_t bar, uint32_t parity) {
-        for (int i = 0; i < 1024; ++i) {
-            if (warp_wait(bar, parity)) return true;
-            if (__any_sync(0xffffffffu, abort_flag != 0)) return false;
-        }
-        return false;
+        return wait_in_slices([&] { return (bool)__all_sync(0xffffffffu, mbar_wait(bar, parity, kPollsASlice)); },
+                              [&] { return (bool)__any_sync(0xffffffffu, abort_flag != 0); });
     };
     // The k-th part of this run; false behind the last one, or where a wait gave up (`ok`).
     auto next_part = [&](int k, Part &s, bool &ok) {
