@@ -268,8 +268,8 @@ prompt_kernel(const PromptParams p, const __grid_constant__ CUtensorMap tmap_q,
     };
     // A wait that may last as long as a unit does; given up early if another role has (kf_wait.cuh).
     auto long_wait = [&](uint32_t bar, uint32_t parity) {
-        return wait_in_slices([&] { return (bool)__all_sync(0xffffffffu, mbar_wait(bar, parity, kPollsASlice)); },
-                              [&] { return (bool)__any_sync(0xffffffffu, abort_flag != 0); });
+        KF_WAIT_IN_SLICES(__all_sync(0xffffffffu, mbar_wait(bar, parity, kPollsASlice)),
+                          __any_sync(0xffffffffu, abort_flag != 0));
     };
     // The k-th unit of this CTA; false behind the last one, or where a wait gave up (`ok`).
     auto next_unit = [&](int k, Unit &u, bool &ok) {

@@ -274,8 +274,8 @@ tree_kernel(const TreeParams p, const Partials part, const __grid_constant__ CUt
     };
     // A wait that may last as long as a part does; given up early if another role has (kf_wait.cuh).
     auto long_wait = [&](uint32_t bar, uint32_t parity) {
-        return wait_in_slices([&] { return (bool)__all_sync(0xffffffffu, mbar_wait(bar, parity, kPollsASlice)); },
-                              [&] { return (bool)__any_sync(0xffffffffu, abort_flag != 0); });
+        KF_WAIT_IN_SLICES(__all_sync(0xffffffffu, mbar_wait(bar, parity, kPollsASlice)),
+                          __any_sync(0xffffffffu, abort_flag != 0));
     };
     // The k-th part of this run; false behind the last one, or where a wait gave up (`ok`).
     auto next_part = [&](int k, Part &s, bool &ok) {

@@ -18,13 +18,15 @@ MODEL = r"""
 int main(int, char **v) {
     const long long comes = atoll(v[1]), stops = atoll(v[2]);
     long long polls = 0;
-    const bool ok = kf::wait_in_slices([&] {
+    auto slice = [&] {
         for (unsigned i = 0; i < kf::kPollsASlice; ++i) {
             ++polls;
             if (comes >= 0 && polls > comes) return true;
         }
         return false;
-    }, [&] { return stops >= 0 && polls >= stops; });
+    };
+    auto wait = [&] { KF_WAIT_IN_SLICES(slice(), stops >= 0 && polls >= stops); };
+    const bool ok = wait();
     printf("%d %lld\n", ok, polls);
 }
 """
@@ -65,6 +67,6 @@ def test_the_kernels_wait_no_longer(name):
     round a bounded wait a fixed number of times."""
     src = re.sub(r"//[^\n]*", "", open(os.path.join(CSRC, name)).read())
     body = re.search(r"auto long_wait = \[&\]\(uint32_t bar, uint32_t parity\) \{(.*?)\n    \};", src, re.S).group(1)
-    assert re.search(r"return wait_in_slices\(.*mbar_wait\(bar, parity, kPollsASlice\).*abort_flag != 0", body, re.S)
+    assert re.search(r"KF_WAIT_IN_SLICES\(.*mbar_wait\(bar, parity, kPollsASlice\).*abort_flag != 0", body, re.S)
     for m in re.finditer(r"for \(int i = 0; i < (\d+); \+\+i\) \{([^}]*)\}", src):
         assert "_wait(" not in m.group(2), m.group(0)
