@@ -757,10 +757,9 @@ kf_status kf_prompt_attention(const void *q, const void *k, const void *v, int64
  * infinity in a row that some node of a request sees can reach that request's other
  * nodes. Scores, softmax statistics and sums are fp32; softmax weights enter the value
  * product as bf16 (E4M3 caches: fp16; for an fp32 out as the sum of three or two such
- * numbers), the sum that normalises them is unrounded. The tensor cores cut fp32 sums off
- * instead of rounding them, which an fp32 out shows where an SM's share of the batch is
- * long: one request of 1000 tokens is off by 8e-7 (relative), 64 of 4096 by 5e-6, 64 of
- * 16384 by 2e-5.
+ * numbers), the sum that normalises them is unrounded. An fp32 out is off by some 1e-6
+ * (relative) at 1000 tokens and by 2e-6 where an SM works on 1000 tokens or more of a
+ * request, whatever their number.
  * The _fp8 call reads E4M3 caches with k_scale, v_scale f32 [num_kv_heads]. Each row of q
  * enters its score product as the sum of two E4M3 numbers times a power of two: numbers
  * below 2^-9 of the row's largest are off by up to 2^-17 of it, the others exact.
@@ -785,8 +784,9 @@ kf_status kf_tree_attention_fp8(const void *q, const int32_t *q_start, const int
                                 float scale, void *workspace, size_t workspace_bytes, void *out,
                                 kf_dtype out_dtype, float *lse_out, kf_stream_t stream);
 
-/* Workspace bytes of kf_tree_attention[_fp8] on the CURRENT device, whatever the batch;
- * 0 if that device cannot be queried or the arguments are invalid. */
+/* Workspace bytes of kf_tree_attention[_fp8] on the CURRENT device, whatever the batch and
+ * the type of out (an fp32 out keeps sums there; a bf16 out needs less); 0 if that device
+ * cannot be queried or the arguments are invalid. */
 size_t kf_tree_workspace_size(int max_query_len, int num_q_heads, int num_kv_heads, int head_dim);
 
 /*

@@ -65,7 +65,9 @@ kf_status tree_impl(const void *q, const int32_t *q_start, const int32_t *parent
     TreeParams p;
     int sms = 0;
     if (device_facts(&p.err, &sms) != cudaSuccess) return KF_ERR_CUDA;
-    if (workspace_bytes < tree_workspace_bytes(nodes, num_q_heads, num_kv_heads, head_dim, sms)) return KF_ERR_INVALID;
+    if (workspace_bytes <
+        tree_workspace_bytes(nodes, num_q_heads, num_kv_heads, head_dim, out_dtype == KF_F32, sms))
+        return KF_ERR_INVALID;
     void *fn = tensor_map_encoder();
     if (!fn) return KF_ERR_CUDA;
     p.q = static_cast<const uint16_t *>(q);
@@ -225,7 +227,7 @@ size_t kf_tree_workspace_size(int max_query_len, int num_q_heads, int num_kv_hea
     unsigned int *err = nullptr;
     int sms = 0;
     if (device_facts(&err, &sms) != cudaSuccess) return 0;
-    return tree_workspace_bytes(std::min(max_query_len, kMaxNodes), num_q_heads, num_kv_heads, head_dim, sms);
+    return tree_workspace_bytes(std::min(max_query_len, kMaxNodes), num_q_heads, num_kv_heads, head_dim, true, sms);
 }
 
 kf_status kf_accept_tree(const int32_t *parents, const int32_t *draft_tokens, const int32_t *target_tokens,

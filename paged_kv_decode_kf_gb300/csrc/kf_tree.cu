@@ -30,8 +30,12 @@
 // Precision: scores and sums fp32; weights enter the value product as bf16 (2^-8 of the
 // weight at most) or fp16 (2^-11; relative to the maximum less 7, which uses the type's range
 // whole); an fp32 output takes them in three pieces of bf16 or two of fp16, as many products
-// into one sum, which the tensor cores cut off at every step (64 requests of 4096 tokens: 4.7e-6
-// against 64 bits; TMEM has no room for a second sum beside two streams).
+// into one sum, which the tensor cores cut off at every step. Every four tiles the softmax warps
+// add it to one of their own, rounded, and clear it. TMEM and shared memory are full, so that sum
+// lies in the workspace, a quad of columns of all rows at a time. 64 requests of 4096, 16384 or
+// 65536 tokens, 16 nodes, are off by 2.0e-6 (E4M3 1.7e-6) against 64 bits, where one sum a run
+// was off by 6e-6, 2.2e-5 and 8e-5; 4096 tokens take 282 us instead of 228 (E4M3 245, 190), 16384 tokens
+// 1007 instead of 815. Every eight tiles: 3.6e-6, 947 us.
 //
 // Bound and measured (32/8 heads of 128). bf16 caches: HBM; 64 requests of 3.5-4K tokens and 16
 // nodes 172 us, 0.88 of the measured copy rate (0.95 where contexts of 1K-32K are long enough to
@@ -64,6 +68,7 @@ constexpr int kRows = 128, kTok = 128;
 __host__ __device__ constexpr int unit_rows(bool kv8) { return kv8 ? kRows : 2 * kRows; }
 constexpr int kLoadWarp = 8, kIssuerWarp = 9, kPlanWarp = 10, kIssuerWarp2 = 11, kStoreWarp = 12, kThreads = 512;
 constexpr int kPlanned = 2;  // parts found ahead
+constexpr int kFlush = 4;    // fp32 outputs: a stream's tiles that the tensor cores sum before their sum is set aside
 // Registers a thread, once the four warpgroups have shared out the 128 each that 512
 // threads start with: the softmax ones hold a row's 128 scores.
 constexpr int kSoftRegs = 176, kOtherRegs = 80;
@@ -112,6 +117,10 @@ struct Partials {
     float *lse;  // [2 * CTAs][pitch]
     Cut *cuts;   // [CTAs]: the unit that starts in CTA i's run and goes on (parts = 0: none)
     int pitch;   // rows a slot holds
+    // fp32 outputs: each CTA's two streams' sums set aside, [2 * CTAs][D / 4][kRows] quads of columns,
+    // and the maxima that they are relative to, [2 * CTAs][kRows]
+    float4 *sums;
+    float *sums_m;
 };
 
 struct Request {
@@ -156,6 +165,21 @@ __device__ __forceinline__ void mma_ss_e4m3(uint32_t d, uint64_t a, uint64_t b, 
         "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
         "l"(a), "l"(b), "r"(idesc), "r"(acc)
         : "memory");
+}
+
+// What other threads of the CTA have left in the workspace, past the first-level cache.
+__device__ __forceinline__ float4 load_l2(const float4 *p) {
+    float4 v;
+    asm volatile("ld.global.cg.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+                 : "l"(p)
+                 : "memory");
+    return v;
+}
+__device__ __forceinline__ float load_l2(const float *p) {
+    float v;
+    asm volatile("ld.global.cg.f32 %0, [%1];" : "=f"(v) : "l"(p) : "memory");
+    return v;
 }
 
 // Four E4M3 codes (lowest byte first) to two fp16 pairs, exactly.
@@ -286,6 +310,8 @@ tree_kernel(const TreeParams p, const Partials part, const __grid_constant__ CUt
         warp_arrive(u_empty(e));
         return s.n >= 0;
     };
+    // F32: stream t's sum set aside for row r
+    auto sums_of = [&](int t, int r) { return part.sums + (int64_t)(2 * run + t) * (D / 4) * kRows + r; };
     auto give_up = [&] {
         if (lane == 0) raise_error(p.err, KF_DEVERR_TIMEOUT);
         abort_flag = 1;
@@ -646,6 +672,7 @@ tree_kernel(const TreeParams p, const Partials part, const __grid_constant__ CUt
             if (bad_row) c = NAN;
             const float cs = c > 0.f ? c : 1.f;  // (a scale of zero or less is applied first)
             float m = -INFINITY, l = 0.f;
+            float aside = -INFINITY;  // F32: the maximum that the sums set aside are relative to
             for (int i = 0; i < tiles; ++i, ++sc) {
                 const int j = alt ? 2 * i + t : i, t0 = (s.tile0 + j) * kTok;
                 if (!long_wait(s_full(t), sc & 1)) {
@@ -669,6 +696,37 @@ tree_kernel(const TreeParams p, const Partials part, const __grid_constant__ CUt
                                      : "memory");
                     }
                     fence_proxy_async_smem();
+                }
+                // (constexpr: a plain condition costs the other forms; E4M3, 64 columns 218 -> 222 us)
+                if constexpr (F32) if (i > 0 && i % kFlush == 0) {  // O, complete up to the tile before, is set aside
+                    float4 *const sums = sums_of(t, r);
+                    auto quad = [&](int at) {
+                        return i > kFlush ? load_l2(sums + at * kRows) : make_float4(0.f, 0.f, 0.f, 0.f);
+                    };
+                    float4 set[16];  // (64 columns on their way at a time)
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) set[e] = quad(e);
+                    const float keep = aside == m ? 1.f : exp2f(aside - m);
+                    aside = m;
+                    const uint32_t zero[16] = {};
+#pragma unroll
+                    for (int cc = 0; cc < D; cc += 16) {
+                        uint32_t o[16];
+                        tmem_ld16(to + cc, o);
+                        tmem_st16_async(to + cc, zero);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            float4 &v = set[(cc / 4 + e) % 16];
+                            v.x = fmaf(v.x, keep, __uint_as_float(o[4 * e]));
+                            v.y = fmaf(v.y, keep, __uint_as_float(o[4 * e + 1]));
+                            v.z = fmaf(v.z, keep, __uint_as_float(o[4 * e + 2]));
+                            v.w = fmaf(v.w, keep, __uint_as_float(o[4 * e + 3]));
+                            __stcg(sums + (cc / 4 + e) * kRows, v);
+                            if (cc + 64 < D) v = quad(cc / 4 + e + 16);
+                        }
+                    }
+                    __stcg(part.sums_m + (2 * run + t) * kRows + r, m);
+                    tmem_wait_st();
                 }
                 uint32_t x[2][64];
                 tmem_ld64_async(ts, x[0]);
@@ -775,6 +833,19 @@ tree_kernel(const TreeParams p, const Partials part, const __grid_constant__ CUt
                     f[1] = 0.f;
                     lse = finish(a.x, a.y);
                 }
+                // F32: what to multiply the sums set aside by (those of the other row tile's rows
+                // lie with stream 1; 0: none)
+                float keep[2] = {0.f, 0.f};
+                if constexpr (F32) {
+                    if (stream_tiles(s, t) > kFlush) {
+                        const float from = load_l2(part.sums_m + (2 * run + t) * kRows + r);
+                        keep[0] = from == a.x ? 1.f : exp2f(from - a.x);
+                    }
+                    if (both && stream_tiles(s, 1) > kFlush) {
+                        const float m = sm_ml[kRows + r].x, from = load_l2(part.sums_m + (2 * run + 1) * kRows + r);
+                        keep[1] = from == m ? 1.f : exp2f(from - m);
+                    }
+                }
                 const int64_t at_row = (int64_t)(s.q0 + s.node0 + (row >> g_shift)) * p.num_q_heads + s.head * G + (r & (G - 1));
                 const int64_t at_part = (int64_t)s.slot * part.pitch + row;
                 if (row_ok) {
@@ -786,6 +857,18 @@ tree_kernel(const TreeParams p, const Partials part, const __grid_constant__ CUt
                     uint32_t o[16], o2[16];
                     tmem_ld16(tw + Sh::col_o(t) + cc, o);
                     if (both) tmem_ld16(tw + Sh::col_o(1) + cc, o2);
+                    auto add_sums = [&](int u, float k, uint32_t (&to)[16]) {
+                        const float4 *const sums = sums_of(u, r) + cc / 4 * kRows;
+                        float4 v[4];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) v[e] = load_l2(sums + e * kRows);
+#pragma unroll
+                        for (int e = 0; e < 16; ++e)
+                            to[e] = __float_as_uint(
+                                fmaf(reinterpret_cast<const float *>(v)[e], k, __uint_as_float(to[e])));
+                    };
+                    if constexpr (F32) if (keep[0] != 0.f) add_sums(t, keep[0], o);
+                    if constexpr (F32) if (keep[1] != 0.f) add_sums(1, keep[1], o2);
                     if (cc == D - 16) {
                         tc05::fence_before_sync();
                         warp_arrive(o_empty(t));
@@ -1109,9 +1192,12 @@ int row_pitch(int max_query_len, int num_q_heads, int num_kv_heads) {
 
 }  // namespace
 
-size_t tree_workspace_bytes(int max_query_len, int num_q_heads, int num_kv_heads, int head_dim, int sm_count) {
-    const size_t rows = 2 * (size_t)sm_count * row_pitch(max_query_len, num_q_heads, num_kv_heads);
-    return al256(rows * head_dim * 4) + al256(rows * 4) + sm_count * sizeof(Cut);
+size_t tree_workspace_bytes(int max_query_len, int num_q_heads, int num_kv_heads, int head_dim, bool f32,
+                            int sm_count) {
+    const int pitch = row_pitch(max_query_len, num_q_heads, num_kv_heads);
+    const size_t rows = 2 * (size_t)sm_count * pitch;
+    const size_t parts = al256(rows * head_dim * 4) + al256(rows * 4) + sm_count * sizeof(Cut);
+    return f32 ? al256(parts) + 2 * (size_t)sm_count * (head_dim + 1) * kRows * sizeof(float) : parts;
 }
 
 cudaError_t launch_tree(const TreeParams &p, void *workspace, int sm_count, cudaStream_t stream, void *encode_fn) {
@@ -1131,20 +1217,23 @@ cudaError_t launch_tree(const TreeParams &p, void *workspace, int sm_count, cuda
     const size_t rows = 2 * (size_t)sm_count * part.pitch;
     uint8_t *ws = static_cast<uint8_t *>(workspace) + al256(rows * p.head_dim * 4);
     part.lse = reinterpret_cast<float *>(ws);
-    part.cuts = reinterpret_cast<Cut *>(ws + al256(rows * 4));
-    const bool pair = p.out_dtype == KF_F32;
+    ws += al256(rows * 4);
+    part.cuts = reinterpret_cast<Cut *>(ws);
+    part.sums = reinterpret_cast<float4 *>(ws + al256(sm_count * sizeof(Cut)));  // (fp32 outputs only)
+    part.sums_m = reinterpret_cast<float *>(part.sums + 2 * (size_t)sm_count * (p.head_dim / 4) * kRows);
+    const bool f32 = p.out_dtype == KF_F32;
     if (p.k_scale) {
         if (p.head_dim == 128)
-            return pair ? launch<128, true, true>(p, part, ctas, units, stream, fn)
-                        : launch<128, false, true>(p, part, ctas, units, stream, fn);
-        return pair ? launch<64, true, true>(p, part, ctas, units, stream, fn)
-                    : launch<64, false, true>(p, part, ctas, units, stream, fn);
+            return f32 ? launch<128, true, true>(p, part, ctas, units, stream, fn)
+                       : launch<128, false, true>(p, part, ctas, units, stream, fn);
+        return f32 ? launch<64, true, true>(p, part, ctas, units, stream, fn)
+                   : launch<64, false, true>(p, part, ctas, units, stream, fn);
     }
     if (p.head_dim == 128)
-        return pair ? launch<128, true, false>(p, part, ctas, units, stream, fn)
-                    : launch<128, false, false>(p, part, ctas, units, stream, fn);
-    return pair ? launch<64, true, false>(p, part, ctas, units, stream, fn)
-                : launch<64, false, false>(p, part, ctas, units, stream, fn);
+        return f32 ? launch<128, true, false>(p, part, ctas, units, stream, fn)
+                   : launch<128, false, false>(p, part, ctas, units, stream, fn);
+    return f32 ? launch<64, true, false>(p, part, ctas, units, stream, fn)
+               : launch<64, false, false>(p, part, ctas, units, stream, fn);
 }
 
 }  // namespace kf

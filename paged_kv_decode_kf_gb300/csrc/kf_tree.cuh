@@ -55,7 +55,7 @@ __device__ __forceinline__ TreeRequest tree_request(const int32_t *q_start, cons
     return {q0, C, L};
 }
 
-size_t tree_workspace_bytes(int max_query_len, int num_q_heads, int num_kv_heads, int head_dim, int sm_count);
+size_t tree_workspace_bytes(int max_query_len, int num_q_heads, int num_kv_heads, int head_dim, bool f32, int sm_count);
 cudaError_t launch_tree(const TreeParams &p, void *workspace, int sm_count, cudaStream_t stream, void *encode_fn);
 
 struct AcceptArgs {
