@@ -105,8 +105,9 @@ __device__ __forceinline__ void store32(void *dst, const uint32_t (&w)[8], bool 
 // tile's 64 weights: 32 columns a piece, one piece behind the other, a half over its own
 // scores; three pieces do not fit there, so both halves take the first 96 columns in turn and
 // `reuse()` waits until the value product has read the first (false where that gave up).
-// Two pieces of bf16 are off by 2^-18 (an fp32 output by 1.8e-6, more than six times what fp32
-// sums cost), three by 2^-27; two of fp16 by 2^-24.
+// Two pieces of bf16 are off by up to 2^-17 of the weight (1 + 2^-9 + 2^-17: the rest of 1 lies half-way
+// between bf16 numbers 2^-16 apart; outputs of 1-1261 tokens were off by 1.8e-6, four times what three
+// take), three hold its 24 bits; two of fp16 are off by up to 2^-23, its last bit.
 // The maximum moves only by more than 8 (base 2); then the row of O (at `to`, if has_o),
 // complete up to the tile before, is rescaled, and that of its low parts (at `to_lo`, if not 0).
 // F16: the weights are fp16, relative to the maximum less 7, so that they use the type's range

@@ -21,6 +21,15 @@ pytestmark = pytest.mark.gpu
 UNIT = 2.0 ** -23
 
 
+def weight_bound(pieces):
+    """How far w / (1 + w) may be off, relatively, w = 2^x of a score known exactly, -4 <= x < 0:
+    ex2.approx 2^-22; x, by the factor's rounding and its own, two half units of 4; what the pieces
+    leave of w, a unit (two of fp16) or nothing; a step for each piece, a unit; the sum of weights, its
+    inverse, the product and the output's rounding, half a unit each. Two pieces of bf16 would be off
+    by up to 2^-17."""
+    return 2 * UNIT + np.log(2) * 4 * UNIT + UNIT + pieces * UNIT + 4 * UNIT / 2
+
+
 @pytest.fixture(scope="module")
 def kf():
     from paged_kv_decode_kf_gb300 import kf
@@ -137,4 +146,131 @@ def test_tree_sums_follow_the_maximum(kf, hq, hkv, d, nodes, fp8, scale):
     run([0], False)
     run([2], False)
     run([7, nan_at, 3], True)
+    assert kf.kf_get_device_error() == 0
+
+
+def exact_scores(n, hq, d, seed, e4m3):
+    """q and k of one component each, whose product is a score of -4 <= scale * log2(e) * s < 0."""
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    q, k = (torch.zeros((n, hq, d), device="cuda") for _ in range(2))
+    q[..., 5] = torch.rand((n, hq), generator=g, device="cuda") + 1
+    k[..., 5] = -torch.rand((n, hq), generator=g, device="cuda") * 1.8 - 0.05
+    if e4m3:
+        k = k.to(torch.float8_e4m3fn).float()
+    return q.to(torch.bfloat16), k.to(torch.bfloat16)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("lead", [0, 77])
+def test_prompt_weights_keep_their_bits(kf, d, lead):
+    """Sequences of two tokens (behind `lead` ones of score 0 and value 0 that weigh nothing like as much
+    where there are any): the second row's output is a weight's."""
+    n, h, scale = 3000, 2, float(np.float32(0.7))
+    q, k = exact_scores(n, h, d, 41, False)
+    g = torch.Generator(device="cuda").manual_seed(42)
+    v = (torch.rand((n, h, d), generator=g, device="cuda") + 1).to(torch.bfloat16)
+    m = lead + 2
+    x = torch.zeros((n, m, 3 * h, d), dtype=torch.bfloat16, device="cuda")
+    x[:, -1, :h], x[:, -1, h:2 * h], x[:, -1, 2 * h:] = q, k, v
+    if lead:          # far below: 2^-40 and less
+        x[:, 1:-1, h:2 * h, 5] = -40.0
+    x = x.view(n * m, 3 * h, d)
+    start = torch.arange(0, n * m + 1, m, dtype=torch.int32, device="cuda")
+    out, _ = kf.kf_prompt_attention(x[:, :h], x[:, h:2 * h], x[:, 2 * h:], start, m, scale, out_dtype=torch.float32)
+    w = torch.exp(scale * (q.double() * k.double()).sum(-1))
+    rest = lead * torch.exp(scale * -40.0 * q[..., 5].double()) if lead else 0.0
+    want = (w / (1 + w + rest))[..., None] * v.double()
+    err = ((out.view(n, m, h, d)[:, -1].double() - want).abs() / want).max()
+    assert err <= weight_bound(3) + (UNIT if lead else 0), float(err)
+    assert kf.kf_get_device_error() == 0
+
+
+@pytest.mark.parametrize("fp8", [False, True], ids=["bf16", "fp8"])
+@pytest.mark.parametrize("d", [64, 128])
+def test_tree_weights_keep_their_bits(kf, d, fp8):
+    """One node behind a context of one token of score 0 and value 0."""
+    n, h, bs, scale = 3000, 2, 16, float(np.float32(0.7))
+    q, k = exact_scores(n, h, d, 43, fp8)
+    v = torch.ones_like(k)
+    kc, vc = (torch.zeros((n, bs, h, d), dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    kc[:, 1], vc[:, 1] = k, v
+    table = torch.arange(n, dtype=torch.int32, device="cuda").view(n, 1)
+    ctx = torch.full((n,), 2, dtype=torch.int32, device="cuda")
+    parents = torch.full((n,), -1, dtype=torch.int32, device="cuda")
+    ws = kf.make_tree_workspace(n, 1, h, h, d)
+    if fp8:
+        kc, vc = (x.to(torch.float8_e4m3fn) for x in (kc, vc))
+        ones = torch.ones(h, device="cuda")
+        out, _ = kf.kf_tree_attention_fp8(q, parents, kc, vc, ones, ones, table, ctx, 2, scale, ws,
+                                          out_dtype=torch.float32)
+    else:
+        out, _ = kf.kf_tree_attention(q, parents, kc, vc, table, ctx, 2, scale, ws, out_dtype=torch.float32)
+    w = torch.exp(scale * (q.double() * k.double()).sum(-1))
+    want = (w / (1 + w))[..., None]
+    err = ((out.double() - want).abs() / want).max()
+    assert err <= weight_bound(2 if fp8 else 3), float(err)
+    assert kf.kf_get_device_error() == 0
+
+
+@pytest.mark.parametrize("lens,hq,hkv,d", [([1000, 300, 1261], 12, 12, 64), ([1000, 300, 1261], 8, 2, 128),
+                                           ([6000], 4, 2, 64), ([6000], 4, 1, 128)])
+def test_prompts_as_near_as_documented(kf, lens, hq, hkv, d):
+    """The error's size over all rows, relative to the output's. Of the 32 steps between two sums set
+    aside each cuts off half a unit on average of a sum that grows by its root (2/3 of the last on
+    average): 10.7 units, 0.72 of it as sums lie between powers of two: 8. Scores lose two units the same way
+    (8 steps or 4), times a size of 1.5: 3. The root of the squares' sum: 8.5 units, 1.02e-6. The three
+    pieces in one sum would be 24 (1.1e-6 and more was measured), sums not set aside more."""
+    g = torch.Generator(device="cuda").manual_seed(44)
+    T = sum(lens)
+    x = torch.randn((T, hq + 2 * hkv, d), generator=g, device="cuda").to(torch.bfloat16)
+    x[:, :hq] *= 1.5
+    q, k, v = x.split([hq, hkv, hkv], 1)
+    ends = np.cumsum(lens)
+    start = torch.tensor([0] + ends.tolist(), dtype=torch.int32, device="cuda")
+    out, _ = kf.kf_prompt_attention(q, k, v, start, max(lens), d ** -0.5, out_dtype=torch.float32)
+    off = size = 0.0
+    for n, e in zip(lens, ends):
+        for r in range(0, n, 1500):
+            m = min(n, r + 1500)
+            seen = torch.ones((m, m), dtype=torch.bool, device="cuda").tril()[r:]
+            o = ref.attend(q[e - n + r:e - n + m].double(), k[e - n:e - n + m].double(), v[e - n:e - n + m].double(), seen,
+                           d ** -0.5)[0]
+            off += float(((out[e - n + r:e - n + m].double() - o) ** 2).sum())
+            size += float((o ** 2).sum())
+    assert (off / size) ** 0.5 <= 8.5 * UNIT, (off / size) ** 0.5
+
+
+@pytest.mark.parametrize("fp8", [False, True], ids=["bf16", "fp8"])
+@pytest.mark.parametrize("d,nodes,L", [(128, 16, 1000), (128, 16, 20000), (64, 40, 20000)])
+def test_trees_as_near_as_documented(kf, d, nodes, L, fp8):
+    """As above; all pieces go into one sum, so that 96 steps (64) lie between two sums set aside: 24
+    units (16); the scores' 3; parts are joined by e^(lse - M), |lse| up to 16: a unit of 16 in a part's
+    weight at most, half a unit on average of two parts: 8. Their root: 25.5 units, 3.0e-6 (18.2, 2.2e-6)."""
+    g = torch.Generator(device="cuda").manual_seed(45)
+    hq, hkv, bs, B = 8, 2, 32, 100
+    blocks = -(-L // bs)
+    k, v = (torch.randn((blocks, bs, hkv, d), generator=g, device="cuda").to(torch.bfloat16) for _ in range(2))
+    scales = [torch.full((hkv,), 1 / 16, device="cuda")] * 2
+    if fp8:
+        k, v = ((x.float() * 16).to(torch.float8_e4m3fn) for x in (k, v))
+    table = torch.arange(blocks, dtype=torch.int32, device="cuda").repeat(B, 1)
+    q = (torch.randn((B * nodes, hq, d), generator=g, device="cuda") * 1.5).to(torch.bfloat16)
+    parents = torch.arange(-1, nodes - 1, dtype=torch.int32, device="cuda").repeat(B)
+    ctx = torch.full((B,), L, dtype=torch.int32, device="cuda")
+    start = torch.arange(0, B * nodes + 1, nodes, dtype=torch.int32, device="cuda")
+    ws = kf.make_tree_workspace(B, nodes, hq, hkv, d)
+    more = dict(q_start=start, max_query_len=nodes, out_dtype=torch.float32)
+    if fp8:
+        out, _ = kf.kf_tree_attention_fp8(q, parents, k, v, *scales, table, ctx, L, d ** -0.5, ws, **more)
+    else:
+        out, _ = kf.kf_tree_attention(q, parents, k, v, table, ctx, L, d ** -0.5, ws, **more)
+    kk, vv = (x.flatten(0, 1)[:L].double() / (16 if fp8 else 1) for x in (k, v))
+    off = size = 0.0
+    for b in (0, 13, B - 1):
+        rows = slice(b * nodes, (b + 1) * nodes)
+        seen = torch.ones((nodes, L), dtype=torch.bool, device="cuda").tril(L - nodes)
+        o = ref.attend(q[rows].double(), kk, vv, seen, d ** -0.5)[0]
+        off += float(((out[rows].double() - o) ** 2).sum())
+        size += float((o ** 2).sum())
+    assert (off / size) ** 0.5 <= (18.2 if fp8 else 25.5) * UNIT, (off / size) ** 0.5
     assert kf.kf_get_device_error() == 0
