@@ -1,4 +1,5 @@
-"""Row ranges that do not ascend: which requests grow, and that no other loses its rows."""
+"""Row ranges that do not ascend: which requests grow, and that no other loses its rows.
+Rows wider than one pass of the kernels that write and move them."""
 import numpy as np
 import pytest
 import torch
@@ -91,3 +92,67 @@ def test_bad_ranges_among_many(kf, batch):
     bad = starts.copy()
     bad[rng.integers(0, batch, 40)] = rng.choice([-1, n + 1, 2 ** 31 - 1], 40)
     extend_and_compare(kf, lens, bad, n)
+
+
+@pytest.mark.parametrize("hkv,d", [(8, 128), (9, 128), (17, 64), (12, 128), (32, 128), (100, 128)])
+@pytest.mark.parametrize("fp8", [False, True], ids=["bf16", "fp8"])
+def test_rows_of_any_width(kf, hkv, d, fp8):
+    """128 vectors of 8 values are a pass of a warp. Slots that are refused leave both caches alone, and
+    the other rows are written."""
+    g = torch.Generator(device="cuda").manual_seed(hkv)
+    n, nb, bs = 61, 5, 16
+    k, v = (torch.randn((n, hkv, d), generator=g, device="cuda").mul_(100).to(torch.bfloat16) for _ in range(2))
+    ks, vs = (torch.rand(hkv, generator=g, device="cuda") + 0.1 for _ in range(2))
+    old = torch.randint(0, 100, (nb, bs, hkv, d), generator=g, device="cuda").to(torch.uint8 if fp8 else torch.bfloat16)
+    held = lambda x, s: (x.float() / s[:, None]).clamp(-448, 448).to(torch.float8_e4m3fn).view(torch.uint8) if fp8 else x
+    good = torch.randperm(nb * bs, generator=g, device="cuda")[:n]
+    for bad in (None, nb * bs, -2, 2 ** 62, -2 ** 63, -1):
+        slots = good.clone()
+        if bad is not None:
+            slots[7] = slots[n - 1] = bad
+        live = slots == good
+        kc, vc, wk, wv = (old.clone() for _ in range(4))
+        wk.view(nb * bs, hkv, d)[slots[live]] = held(k, ks)[live]
+        wv.view(nb * bs, hkv, d)[slots[live]] = held(v, vs)[live]
+        if fp8:
+            kf.kf_append_rows_fp8(k, v, kc, vc, ks, vs, slots)
+        else:
+            kf.kf_append_rows(k, v, kc, vc, slots)
+        assert torch.equal(kc, wk) and torch.equal(vc, wv), bad
+        assert kf.kf_get_device_error() == (0 if bad in (None, -1) else kf.KF_DEVERR_APPEND_POS)
+
+
+@pytest.mark.parametrize("row_bytes", [16, 2032, 2048, 2064, 4112, 8192, 1 << 16])
+@pytest.mark.parametrize("two", [False, True])
+def test_commits_of_rows_of_any_width(kf, row_bytes, two):
+    """128 vectors of 16 bytes are a pass of a block; a path that turns bad does so for every pass."""
+    g = torch.Generator(device="cuda").manual_seed(row_bytes)
+    nb, bs = 40, 16
+    nodes = [30, 12, 20, 1, 9]
+    lens = [60, 12, 100, 33, 20]
+    # the second leaves the nodes, the third repeats one
+    paths = [[0, 2, 3, 8, 9, 10, 15, 16, 20, 29], [0, 1, 11, 12, 13], [0, 5, 6, 6, 7], [0], [3, 8]]
+    kept = [10, 3, 3, 1, 2]
+    table = torch.full((5, 8), -1, dtype=torch.int32, device="cuda")
+    ids, at = torch.randperm(nb, generator=g, device="cuda").to(torch.int32), 0
+    for b, n in enumerate(lens):
+        need = -(-n // bs)
+        table[b, :need] = ids[at:at + need]
+        at += need
+    path = torch.full((5, 12), -1, dtype=torch.int32, device="cuda")
+    for b, p in enumerate(paths):
+        path[b, :len(p)] = i32(p)
+    caches = [torch.randint(0, 256, (nb, bs, row_bytes), generator=g, device="cuda").to(torch.uint8)
+              for _ in range(1 + two)]
+    want = [c.clone() for c in caches]
+    slot = lambda b, t: int(table[b, t // bs]) * bs + t % bs
+    for c, w in zip(caches, want):
+        for b, p in enumerate(paths):
+            first = lens[b] - nodes[b]
+            for i in range(kept[b]):
+                w.view(nb * bs, -1)[slot(b, first + i)] = c.view(nb * bs, -1)[slot(b, first + p[i])]
+    start = i32(np.concatenate([[0], np.cumsum(nodes)]))
+    kf.kf_commit_tree(caches, table, i32(lens), start, path, i32([len(p) for p in paths]))
+    assert kf.kf_get_device_error() == kf.KF_DEVERR_TREE
+    for c, w in zip(caches, want):
+        assert torch.equal(c, w)
