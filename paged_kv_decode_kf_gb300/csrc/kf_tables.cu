@@ -16,10 +16,10 @@
 // Rows are the unit of work: a row finds its request and from off_b its block, and the
 // row at a new block's first position (every new block has one) writes the table entry.
 // So no CTA waits for another: each finds the ends and the needs of the whole batch by itself
-// (three words a request, from L2), which replaces a launch between the sums and the rows: extend and
-// release together 7.3 us for 64 requests of one row, 8.2 for 33 prompts of 37000 rows. The
-// last CTA to finish (a ticket in the pool's header) moves the pool's count and writes
-// the lengths, which may overwrite those that the others read.
+// (three words a request, from L2), which replaces a launch between the sums and the rows:
+// extend and release together 6.0 us for 64 requests of one row, 8.3 for 33 prompts of 33500
+// rows. The last CTA to finish (a ticket in the pool's header) moves the pool's count and
+// writes the lengths, which may overwrite those that the others read.
 #include "kf_tables.cuh"
 
 #include <algorithm>
@@ -84,8 +84,9 @@ __device__ __forceinline__ int64_t freed_of(const PoolArgs &a, int b, bool repor
     return ((len + a.block_size - 1) >> shift) - keep;
 }
 
-// The sum of every thread's `mine` over the threads before it; `total` of all.
-__device__ __forceinline__ int64_t scan_before(int64_t mine, int64_t *sm_warp, int64_t &total) {
+// The sum of every thread's `mine` over the threads before it; `total` of all. `any`: whether
+// it is true in some thread.
+__device__ __forceinline__ int64_t scan_before(int64_t mine, int64_t *sm_warp, int64_t &total, bool &any) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     int64_t v = mine;
     for (int o = 1; o < 32; o <<= 1) {
@@ -93,7 +94,7 @@ __device__ __forceinline__ int64_t scan_before(int64_t mine, int64_t *sm_warp, i
         if (lane >= o) v += y;
     }
     if (lane == 31) sm_warp[warp] = v;
-    __syncthreads();
+    any = __syncthreads_or(any);
     int64_t before = v - mine;
     total = 0;
     for (int w = 0; w < kThreads / 32; ++w) {
@@ -150,19 +151,30 @@ extend_kernel(const PoolArgs a) {
     __shared__ unsigned long long sm_taken;
     __shared__ int sm_last;
     const int tid = threadIdx.x;
-    const bool report = blockIdx.x == 0;
     const int per = (a.batch + kThreads - 1) / kThreads;  // requests a thread
     const int chunks = (a.batch + per - 1) / per;
     const int b0 = min(tid * per, a.batch), b1 = min(b0 + per, a.batch);
-    const int64_t free = free_of(a, report && tid == 0);
-    int64_t mine = 0, total, last = 0, s, e;
-    for (int b = b0; b < b1; ++b)
-        if (rows_of(a, b, s, e)) last = max(last, e);
-    const int64_t ahead = max_before(last, sm_warp_end);
-    sm_end[tid] = ahead;
+    const int64_t free = free_of(a, blockIdx.x == 0 && tid == 0);
+    // Where no range leaves the rows they ascend, and a request's start is the largest end ahead of it.
+    int64_t ahead = 0, mine = 0, total, s, e;
+    bool bad = false;
+    if (b0 < b1) rows_of(a, b0, ahead, e);
     int64_t end = ahead;
-    for (int b = b0; b < b1; ++b) mine += need_of(a, b, report, end).blocks;
-    sm_off[tid] = scan_before(mine, sm_warp, total);
+    for (int b = b0; b < b1; ++b) {
+        bad = bad || !rows_of(a, b, s, e);
+        mine += need_of(a, b, false, end).blocks;
+    }
+    sm_off[tid] = scan_before(mine, sm_warp, total, bad);
+    if (bad) {  // (in all threads) else it has to be found
+        int64_t last = 0;
+        for (int b = b0; b < b1; ++b)
+            if (rows_of(a, b, s, e)) last = max(last, e);
+        ahead = end = max_before(last, sm_warp_end);
+        mine = 0;
+        for (int b = b0; b < b1; ++b) mine += need_of(a, b, false, end).blocks;
+        sm_off[tid] = scan_before(mine, sm_warp, total, bad);
+    }
+    sm_end[tid] = ahead;
     if (tid == 0) sm_taken = 0;
     __syncthreads();
 
@@ -203,7 +215,7 @@ extend_kernel(const PoolArgs a) {
     bool short_of = false;
     end = ahead;
     for (int b = b0; b < b1; ++b) {
-        const Need n = need_of(a, b, false, end);
+        const Need n = need_of(a, b, true, end);
         const bool fits = off + n.blocks <= free;
         off += n.blocks;
         if (fits) taken = off;
@@ -233,7 +245,8 @@ release_kernel(const PoolArgs a) {
     int64_t mine = 0, keep;
     for (int b = b0; b < b1; ++b) mine += freed_of(a, b, report, keep);
     int64_t total;
-    sm_off[tid] = scan_before(mine, sm_warp, total);
+    bool none = false;
+    sm_off[tid] = scan_before(mine, sm_warp, total, none);
     __syncthreads();
     const bool fits = free + total <= a.num_blocks;  // else some block is in the list already
     if (!fits && report && tid == 0) raise_error(a.err, KF_DEVERR_POOL);
@@ -284,7 +297,8 @@ pool_init_kernel(int32_t *pool, int64_t num_blocks) {
 // of 8 x 128 into E4M3 caches 40.1 us, 5.7 TB/s of reads and writes.
 //
 // E4M3: the code of x / s, eight numbers of a head at a time. The division itself costs more
-// issue slots than HBM leaves (16 a number, most of them its; 48.5 us), so the quotient is Markstein's (IBM Journal of Research and Development 34, 1990,
+// issue slots than HBM leaves (16 a number; 48.5 us), so the quotient is Markstein's (IBM
+// Journal of Research and Development 34, 1990,
 // 111-119): with y = 1 / s rounded, q = x y, r = x - q s, q' = q + r y. Its error ahead of the
 // last rounding is below 2^-22 of a unit in the last place. A code can only differ from the
 // exact division's if x / s is that near to half a unit beside a border M of two codes (16 <= M
