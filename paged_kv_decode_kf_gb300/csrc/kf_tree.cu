@@ -41,8 +41,8 @@
 // nodes 172 us, 0.88 of the measured copy rate (0.95 where contexts of 1K-32K are long enough to
 // hide the start and the merge); 61 nodes 248, one request of 32K 38.6, 24/24 heads of 64 282.
 // E4M3 caches: 64 of 1K-64K tokens, 32 nodes 520 us, 0.55 of HBM: two streams of 128 rows finish a
-// tile each in some 4000 cycles (scores, softmax, widening, value product, hand-offs), and a
-// part's start and end are 10000 or more; 64 of 3.5-4K, 16 nodes 147. Eight requests of 2-16K, 61
+// tile each in some 5000 cycles (scores, softmax, widening, value product, hand-offs; 389 tiles a
+// CTA), a part's start and end among them; 64 of 3.5-4K, 16 nodes 147. Eight requests of 2-16K, 61
 // nodes, 64/8 heads 128 us, half of the tensor rate: 488 rows are two units of 256, whose second
 // is not full, and a softmax tile is longer than its products. One issuer for both streams took
 // 179 us instead of 172 and 163 instead of 128.
