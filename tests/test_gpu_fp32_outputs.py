@@ -274,3 +274,43 @@ def test_trees_as_near_as_documented(kf, d, nodes, L, fp8):
         size += float((o ** 2).sum())
     assert (off / size) ** 0.5 <= (18.2 if fp8 else 25.5) * UNIT, (off / size) ** 0.5
     assert kf.kf_get_device_error() == 0
+
+
+def test_tree_sums_captured_and_on_streams(kf):
+    """Sums set aside lie in the call's workspace: replayed graphs with other lengths, and four streams
+    with a workspace each, give the bits of a call alone."""
+    g = torch.Generator(device="cuda").manual_seed(46)
+    hq, hkv, d, bs, C, L = 8, 2, 128, 16, 20, 6000
+    B, blocks = 90, 6000 // 16
+    k, v = (torch.randn((blocks, bs, hkv, d), generator=g, device="cuda").to(torch.bfloat16) for _ in range(2))
+    table = torch.arange(blocks, dtype=torch.int32, device="cuda").repeat(B, 1)
+    q = (torch.randn((B * C, hq, d), generator=g, device="cuda") * 1.5).to(torch.bfloat16)
+    parents = torch.arange(-1, C - 1, dtype=torch.int32, device="cuda").repeat(B)
+    start = torch.arange(0, B * C + 1, C, dtype=torch.int32, device="cuda")
+    lens = [torch.randint(C, L, (B,), generator=g, device="cuda", dtype=torch.int32) for _ in range(4)]
+    spaces = [kf.make_tree_workspace(B, C, hq, hkv, d) for _ in range(4)]
+
+    def call(ctx, ws, out=None, lse=None):
+        return kf.kf_tree_attention(q, parents, k, v, table, ctx, L, d ** -0.5, ws, q_start=start, max_query_len=C,
+                                    out=out, lse_out=lse, out_dtype=torch.float32)
+
+    want = [call(n, spaces[0]) for n in lens]
+    ctx, out, lse = lens[0].clone(), torch.empty_like(want[0][0]), torch.empty_like(want[0][1])
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call(ctx, spaces[0], out, lse)
+    for n, (o, l) in zip(lens, want):
+        ctx.copy_(n)
+        graph.replay()
+        assert torch.equal(out, o) and torch.equal(lse, l)
+    streams = [torch.cuda.Stream() for _ in range(4)]
+    torch.cuda.synchronize()
+    got = []
+    for _ in range(6):
+        for s, ws, n in zip(streams, spaces, lens):
+            with torch.cuda.stream(s):
+                got.append(call(n, ws))
+    torch.cuda.synchronize()
+    for i, (o, l) in enumerate(got):
+        assert torch.equal(o, want[i % 4][0]) and torch.equal(l, want[i % 4][1])
+    assert kf.kf_get_device_error() == 0
