@@ -880,10 +880,10 @@ kf_status kf_init_block_pool(int32_t *pool, int64_t num_blocks, kf_stream_t stre
  * including it need; one that does not keeps its length and table (KF_DEVERR_POOL), as
  * does one whose rows leave its table (KF_DEVERR_APPEND_POS) or whose length or range is
  * bad (KF_DEVERR_CONTEXT_LEN: a range that leaves the rows, or starts before the end of an
- * earlier one that does not); the others grow as if it had no rows. A table or pool entry outside [0,
- * num_blocks) gives slot -1 (KF_DEVERR_BLOCK_ID). Host errors: null or misaligned
- * pointers, negative sizes -> KF_ERR_INVALID; block_size other than 16 or 32 ->
- * KF_ERR_UNSUPPORTED.
+ * earlier one that does not); the others grow as if it had no rows. A table or pool
+ * entry outside [0, num_blocks) gives slot -1 (KF_DEVERR_BLOCK_ID). Host errors: null or
+ * misaligned pointers, negative sizes -> KF_ERR_INVALID; block_size other than 16 or 32
+ * -> KF_ERR_UNSUPPORTED.
  */
 kf_status kf_extend_block_tables(int32_t *pool, int64_t num_blocks, int32_t *block_tables,
                                  int bt_stride, const int32_t *context_lens_before,

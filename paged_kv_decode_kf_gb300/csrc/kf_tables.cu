@@ -298,9 +298,8 @@ pool_init_kernel(int32_t *pool, int64_t num_blocks) {
 //
 // E4M3: the code of x / s, eight numbers of a head at a time. The division itself costs more
 // issue slots than HBM leaves (16 a number; 48.5 us), so the quotient is Markstein's (IBM
-// Journal of Research and Development 34, 1990,
-// 111-119): with y = 1 / s rounded, q = x y, r = x - q s, q' = q + r y. Its error ahead of the
-// last rounding is below 2^-22 of a unit in the last place. A code can only differ from the
+// Journal of Research and Development 34, 1990, 111-119): with y = 1 / s rounded, q = x y,
+// r = x - q s, q' = q + r y. Its error ahead of the last rounding is below 2^-22 of a unit in the last place. A code can only differ from the
 // exact division's if x / s is that near to half a unit beside a border M of two codes (16 <= M
 // <= 31 and a whole number, scaled). With s = S / 2^k, 2^23 <= S < 2^24, x's eight bits make x
 // 2^j - M S a whole number n, |n| within 2^-17 of S / 2^20, 8 <= n <= 16: so S = 2^20 n + t, |t| <= 8,
